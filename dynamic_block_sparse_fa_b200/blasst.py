@@ -123,6 +123,33 @@ _lib.blasst_decode_wide_splits.restype = _i
 _lib.blasst_decode_wide_splits.argtypes = [_i, _i, _i, _i]
 _lib.blasst_decode_group_splits.restype = _i
 _lib.blasst_decode_group_splits.argtypes = [_i, _i, _i, _i, _i]
+_ll = ctypes.c_longlong
+_lib.blasst_block_means.restype = _i
+_lib.blasst_block_means.argtypes = [_vp, _vp, _i, _i, _i, _i, _vp]
+_lib.blasst_block_means_paged.restype = _i
+_lib.blasst_block_means_paged.argtypes = [_vp, _ll, _i, _i, _vp, _i, _vp, _i,
+                                          _i, _vp, _i, _i, _i, _i, _vp]
+_lib.blasst_block_select.restype = _i
+_lib.blasst_block_select.argtypes = [_vp, _vp, _vp] + [_i] * 10 + [_vp]
+_lib.blasst_block_select_decode.restype = _i
+_lib.blasst_block_select_decode.argtypes = ([_vp, _vp, _vp, _i, _i, _vp]
+                                            + [_i] * 7 + [_vp])
+_lib.blasst_select_prefill_workspace_size.restype = _sz
+_lib.blasst_select_prefill_workspace_size.argtypes = [_i] * 5
+_lib.blasst_select_prefill.restype = _i
+_lib.blasst_select_prefill.argtypes = ([_vp] * 6 + [_i] * 7
+                                       + [_f, _i, _vp, _sz, _vp])
+_lib.blasst_select_prefill_backward_workspace_size.restype = _sz
+_lib.blasst_select_prefill_backward_workspace_size.argtypes = [_i] * 6
+_lib.blasst_select_prefill_backward.restype = _i
+_lib.blasst_select_prefill_backward.argtypes = ([_vp] * 10 + [_i] * 7
+                                                + [_f, _i, _vp, _sz, _vp])
+_lib.blasst_select_decode_splits.restype = _i
+_lib.blasst_select_decode_splits.argtypes = [_i] * 4
+_lib.blasst_select_decode_paged.restype = _i
+_lib.blasst_select_decode_paged.argtypes = [_vp, _vp, _vp, _ll, _i, _i, _vp,
+                                            _i, _vp, _i, _vp, _i, _vp, _vp, _i,
+                                            _i, _i, _i, _f, _i, _vp, _sz, _vp]
 _lib.blasst_calibrate.restype = _i
 _lib.blasst_calibrate.argtypes = [_d, ctypes.POINTER(CalibSample), _d, _vp,
                                   ctypes.POINTER(CalibResult), _vp]
@@ -145,7 +172,14 @@ EXPORTED = ["blasst_prefill", "blasst_decode", "blasst_decode_noalloc",
             "blasst_decode_paged",
             "blasst_decode_workspace_size",
             "blasst_decode_splits", "blasst_decode_wide_splits",
-            "blasst_decode_group_splits", "blasst_calibrate", "blasst_fit_a",
+            "blasst_decode_group_splits",
+            "blasst_block_means", "blasst_block_means_paged",
+            "blasst_block_select", "blasst_block_select_decode",
+            "blasst_select_prefill", "blasst_select_prefill_workspace_size",
+            "blasst_select_prefill_backward",
+            "blasst_select_prefill_backward_workspace_size",
+            "blasst_select_decode_paged", "blasst_select_decode_splits",
+            "blasst_calibrate", "blasst_fit_a",
             "blasst_skip_stats_reset", "blasst_check_device_error",
             "blasst_selftest_wait_timeout",
             "blasst_strerror", "blasst_last_error", "blasst_version"]
@@ -655,3 +689,289 @@ def blasst_fit_a(lambdas, lengths) -> float:
     la = (ctypes.c_double * n)(*lambdas)
     le = (ctypes.c_int * n)(*lengths)
     return float(_lib.blasst_fit_a(n, la, le))
+
+
+# ---------------------------------------------------------------------------
+# Block-selected attention
+# ---------------------------------------------------------------------------
+SELECT_BLOCK = 64  # tokens per selection block (BLASST_SELECT_BLOCK)
+
+
+def _nblk(L):
+    return -(-L // SELECT_BLOCK)
+
+
+def _shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected "
+                         f"{tuple(shape)}")
+
+
+def _device(*tensors):
+    """The one device all tensor arguments live on (None entries skipped)."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"tensors on several devices: {sorted(map(str, devs))}")
+    dev = devs.pop()
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device (got {dev})")
+    return dev
+
+
+def _disjoint(outs, ins):
+    """Outputs (name, tensor) must not overlap an input or one another."""
+    for x, (name, t) in enumerate(outs):
+        for other, u in ins + outs[x + 1:]:
+            if _overlaps(t, u):
+                raise ValueError(f"{name} overlaps {other}")
+
+
+def _pool(k_pages, v_pages=None):
+    """(num_pages, Hkv, page_size, d, page stride) of a page pool's views."""
+    P, Hkv, ps, d = k_pages.shape
+    for t in (k_pages, v_pages):
+        if t is None:
+            continue
+        if tuple(t.shape) != (P, Hkv, ps, d):
+            raise ValueError("k_pages / v_pages shapes")
+        if t.stride()[1:] != (ps * d, d, 1):
+            raise ValueError("pages must be contiguous inside a page")
+        if P > 1 and t.stride(0) != k_pages.stride(0):
+            raise ValueError("k_pages and v_pages must share the page stride")
+    # (the stride of a pool of one page means nothing and may be any number)
+    return P, Hkv, ps, d, k_pages.stride(0) if P > 1 else Hkv * ps * d
+
+
+def blasst_block_means(k, *, means=None, stream=None):
+    """Mean of every 64-key block: k [B,Hkv,L,d] bf16 -> [B,Hkv,nblk,d]."""
+    B, Hkv, L, d = k.shape
+    dev = _device(k, means)
+    if means is None:
+        means = torch.empty(B, Hkv, _nblk(L), d, dtype=k.dtype, device=dev)
+    _shape(means, "means", (B, Hkv, _nblk(L), d))
+    _disjoint([("means", means)], [("k", k)])
+    with torch.cuda.device(dev):
+        _check(_lib.blasst_block_means(_arg(k, "k"), _arg(means, "means"), B,
+                                       Hkv, L, d, _stream(stream)),
+               "blasst_block_means")
+    return means
+
+
+def blasst_block_means_paged(k_pages, block_table, seq_lens, means, *,
+                             max_seq_len=None, n_new=0, stream=None):
+    """Bring ``means`` [B,Hkv,max_blocks,d] (updated in place and returned) up
+    to date with a paged cache: the blocks that hold the last ``n_new`` tokens
+    of each sequence, or every block for n_new = 0.  Pool, table and lengths
+    as blasst_decode_paged; max_seq_len: host upper bound on the lengths
+    (default: what the table and ``means`` hold)."""
+    P, Hkv, ps, d, stride = _pool(k_pages)
+    dev = _device(k_pages, block_table, seq_lens, means)
+    B, mp = block_table.shape
+    nb = means.shape[2]
+    _shape(seq_lens, "seq_lens", (B,))
+    _shape(means, "means", (B, Hkv, nb, d))
+    _disjoint([("means", means)], [("block_table", block_table),
+                                   ("seq_lens", seq_lens)])
+    if max_seq_len is None:
+        max_seq_len = min(mp * ps, nb * SELECT_BLOCK)
+    with torch.cuda.device(dev):
+        _check(_lib.blasst_block_means_paged(
+            _arg(k_pages, "k_pages", contiguous=False), stride, P, ps,
+            _arg(block_table, "block_table", torch.int32), mp,
+            _arg(seq_lens, "seq_lens", torch.int32), int(max_seq_len),
+            int(n_new), _arg(means, "means"), nb, B, Hkv, d, _stream(stream)),
+            "blasst_block_means_paged")
+    return means
+
+
+def blasst_block_select(q, means, Lkv, *, n_sel, n_first=1, n_local=1,
+                        causal=True, sel=None, stream=None):
+    """The n_sel key blocks every row of q [B,Hq,Lq,d] attends to, from the
+    block means [B,Hkv,nblk,d] of its Lkv keys: int32 [B,Hkv,Lq,n_sel],
+    ascending, -1 in unused slots.  The first n_first and the last n_local
+    visible blocks are always taken, the others by score."""
+    B, Hq, Lq, d = q.shape
+    Hkv = means.shape[1]
+    dev = _device(q, means, sel)
+    _shape(means, "means", (B, Hkv, _nblk(Lkv), d))
+    if sel is None:
+        sel = torch.empty(B, Hkv, Lq, max(int(n_sel), 0), dtype=torch.int32,
+                          device=dev)
+    _shape(sel, "sel", (B, Hkv, Lq, n_sel))
+    _disjoint([("sel", sel)], [("q", q), ("means", means)])
+    with torch.cuda.device(dev):
+        _check(_lib.blasst_block_select(
+            _arg(q, "q"), _arg(means, "means"), _arg(sel, "sel", torch.int32),
+            B, Hq, Hkv, Lq, int(Lkv), d, int(bool(causal)), int(n_sel),
+            int(n_first), int(n_local), _stream(stream)),
+            "blasst_block_select")
+    return sel
+
+
+def blasst_block_select_decode(q, means, seq_lens, *, n_sel, n_first=1,
+                               n_local=1, max_seq_len=None, sel=None,
+                               stream=None):
+    """blasst_block_select for one token per sequence: q [B,Hq,d], means
+    [B,Hkv,max_blocks,d], seq_lens [B] int32 -> int32 [B,Hkv,n_sel]."""
+    B, Hq, d = q.shape
+    Hkv, nb = means.shape[1], means.shape[2]
+    dev = _device(q, means, seq_lens, sel)
+    _shape(means, "means", (B, Hkv, nb, d))
+    _shape(seq_lens, "seq_lens", (B,))
+    if sel is None:
+        sel = torch.empty(B, Hkv, max(int(n_sel), 0), dtype=torch.int32,
+                          device=dev)
+    _shape(sel, "sel", (B, Hkv, n_sel))
+    _disjoint([("sel", sel)], [("q", q), ("means", means),
+                               ("seq_lens", seq_lens)])
+    if max_seq_len is None:
+        max_seq_len = nb * SELECT_BLOCK
+    with torch.cuda.device(dev):
+        _check(_lib.blasst_block_select_decode(
+            _arg(q, "q"), _arg(means, "means"),
+            _arg(seq_lens, "seq_lens", torch.int32), int(max_seq_len), nb,
+            _arg(sel, "sel", torch.int32), B, Hq, Hkv, d, int(n_sel),
+            int(n_first), int(n_local), _stream(stream)),
+            "blasst_block_select_decode")
+    return sel
+
+
+def blasst_select_prefill_workspace_size(B, Hq, Hkv, Lq, Lkv) -> int:
+    return int(_lib.blasst_select_prefill_workspace_size(B, Hq, Hkv, Lq, Lkv))
+
+
+def blasst_select_prefill_backward_workspace_size(B, Hq, Hkv, Lq, Lkv,
+                                                  d=128) -> int:
+    return int(_lib.blasst_select_prefill_backward_workspace_size(
+        B, Hq, Hkv, Lq, Lkv, d))
+
+
+def blasst_select_decode_splits(B, Hq, Hkv, n_sel) -> int:
+    return int(_lib.blasst_select_decode_splits(B, Hq, Hkv, n_sel))
+
+
+def blasst_select_prefill(q, k, v, sel, *, scale=None, causal=True, o=None,
+                          lse=None, want_lse=True, workspace=None,
+                          stream=None):
+    """Attention over the selected key blocks.  q [B,Hq,Lq,d], k/v
+    [B,Hkv,Lkv,d] bf16, sel [B,Hkv,Lq,n_sel] int32 block ids (any order, -1
+    for none).  Returns (o, lse)."""
+    B, Hq, Lq, d = q.shape
+    Hkv, Lkv = k.shape[1], k.shape[2]
+    dev = _device(q, k, v, sel, o, lse, workspace)
+    _shape(k, "k", (B, Hkv, Lkv, d))
+    _shape(v, "v", k.shape)
+    n_sel = sel.shape[-1]
+    _shape(sel, "sel", (B, Hkv, Lq, n_sel))
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    o = torch.empty_like(q) if o is None else o
+    _shape(o, "o", q.shape)
+    if lse is None and want_lse:
+        lse = torch.empty(B, Hq, Lq, dtype=torch.float32, device=dev)
+    if lse is not None:
+        _shape(lse, "lse", (B, Hq, Lq))
+    if workspace is None:
+        need = blasst_select_prefill_workspace_size(B, Hq, Hkv, Lq, Lkv)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _disjoint([("o", o), ("lse", lse), ("workspace", workspace)],
+              [("q", q), ("k", k), ("v", v), ("sel", sel)])
+    with torch.cuda.device(dev):
+        _check(_lib.blasst_select_prefill(
+            _arg(q, "q"), _arg(k, "k"), _arg(v, "v"),
+            _arg(sel, "sel", torch.int32), _arg(o, "o"),
+            _arg(lse, "lse", torch.float32), B, Hq, Hkv, Lq, Lkv, d, n_sel,
+            float(scale), int(bool(causal)), _arg(workspace, "workspace", None),
+            workspace.numel() * workspace.element_size(), _stream(stream)),
+            "blasst_select_prefill")
+    return o, lse
+
+
+def blasst_select_prefill_backward(q, k, v, o, lse, dout, sel, *, scale=None,
+                                   causal=True, dq=None, dk=None, dv=None,
+                                   workspace=None, stream=None):
+    """Gradients (dq, dk, dv) of a blasst_select_prefill forward with its
+    selection held fixed (d = 128); o and lse are that forward's."""
+    B, Hq, Lq, d = q.shape
+    Hkv, Lkv = k.shape[1], k.shape[2]
+    dev = _device(q, k, v, o, lse, dout, sel, dq, dk, dv, workspace)
+    n_sel = sel.shape[-1]
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    for name, t, shape in (
+            ("k", k, (B, Hkv, Lkv, d)), ("v", v, k.shape), ("o", o, q.shape),
+            ("dout", dout, q.shape), ("lse", lse, (B, Hq, Lq)),
+            ("sel", sel, (B, Hkv, Lq, n_sel)), ("dq", dq, q.shape),
+            ("dk", dk, k.shape), ("dv", dv, k.shape)):
+        _shape(t, name, shape)
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if workspace is None:
+        need = blasst_select_prefill_backward_workspace_size(B, Hq, Hkv, Lq,
+                                                             Lkv, d)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _disjoint([("dq", dq), ("dk", dk), ("dv", dv), ("workspace", workspace)],
+              [("q", q), ("k", k), ("v", v), ("o", o), ("lse", lse),
+               ("dout", dout), ("sel", sel)])
+    with torch.cuda.device(dev):
+        _check(_lib.blasst_select_prefill_backward(
+            _arg(q, "q"), _arg(k, "k"), _arg(v, "v"), _arg(o, "o"),
+            _arg(dout, "dout"), _arg(lse, "lse", torch.float32),
+            _arg(sel, "sel", torch.int32), _arg(dq, "dq"), _arg(dk, "dk"),
+            _arg(dv, "dv"), B, Hq, Hkv, Lq, Lkv, d, n_sel, float(scale),
+            int(bool(causal)), _arg(workspace, "workspace", None),
+            workspace.numel() * workspace.element_size(), _stream(stream)),
+            "blasst_select_prefill_backward")
+    return dq, dk, dv
+
+
+def blasst_select_decode_paged(q, k_pages, v_pages, block_table, seq_lens, sel,
+                               *, max_seq_len=None, scale=None, num_splits=0,
+                               o=None, lse=None, want_lse=True, workspace=None,
+                               stream=None):
+    """One token per sequence over the selected blocks of a paged cache:
+    arguments as blasst_decode_paged, sel [B,Hkv,n_sel] int32 block ids (any
+    order, -1 for none).  Returns (o, lse).  Bad lengths, page ids and block
+    ids are caught on the device: see blasst_check_device_error()."""
+    B, Hq, d = q.shape
+    P, Hkv, ps, d2, stride = _pool(k_pages, v_pages)
+    dev = _device(q, k_pages, v_pages, block_table, seq_lens, sel, o, lse,
+                  workspace)
+    if d2 != d:
+        raise ValueError(f"pages: head dimension {d2}, q has {d}")
+    mp = block_table.shape[1]
+    n_sel = sel.shape[-1]
+    _shape(block_table, "block_table", (B, mp))
+    _shape(seq_lens, "seq_lens", (B,))
+    _shape(sel, "sel", (B, Hkv, n_sel))
+    if max_seq_len is None:
+        max_seq_len = mp * ps
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    o = torch.empty_like(q) if o is None else o
+    _shape(o, "o", q.shape)
+    if lse is None and want_lse:
+        lse = torch.empty(B, Hq, dtype=torch.float32, device=dev)
+    if lse is not None:
+        _shape(lse, "lse", (B, Hq))
+    S = (num_splits if num_splits > 0
+         else blasst_select_decode_splits(B, Hq, Hkv, n_sel))
+    if workspace is None:
+        need = blasst_decode_workspace_size(B, Hq, d, S)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _disjoint([("o", o), ("lse", lse), ("workspace", workspace)],
+              [("q", q), ("block_table", block_table), ("seq_lens", seq_lens),
+               ("sel", sel)])
+    with torch.cuda.device(dev):
+        _check(_lib.blasst_select_decode_paged(
+            _arg(q, "q"), _arg(k_pages, "k_pages", contiguous=False),
+            _arg(v_pages, "v_pages", contiguous=False), stride, P, ps,
+            _arg(block_table, "block_table", torch.int32), mp,
+            _arg(seq_lens, "seq_lens", torch.int32), int(max_seq_len),
+            _arg(sel, "sel", torch.int32), n_sel, _arg(o, "o"),
+            _arg(lse, "lse", torch.float32), B, Hq, Hkv, d, float(scale), S,
+            _arg(workspace, "workspace", None),
+            workspace.numel() * workspace.element_size(), _stream(stream)),
+            "blasst_select_decode_paged")
+    return o, lse

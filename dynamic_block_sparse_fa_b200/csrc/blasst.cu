@@ -15,6 +15,9 @@
 #include "mla.cuh"
 #include "decode_wide.cuh"
 #include "decode_mma.cuh"
+#include "block_select.cuh"
+#include "select_attn.cuh"
+#include "select_bwd.cuh"
 
 namespace {
 
@@ -108,6 +111,13 @@ blasst_status_t blasst_check_device_error(int* where_out) {
              "paged decode: sequence %u has length %d, outside [0, "
              "max_seq_len]",
              info[1], (int)info[2]);
+    return BLASST_ERR_INVALID_ARG;
+  }
+  if (code == blasst::kBadBlockId) {
+    snprintf(g_last_error, sizeof g_last_error,
+             "block selection: list of (sequence, KV head) %u, row %d holds "
+             "block id %d, past the last block",
+             info[1], (int)info[2] < 0 ? 0 : (int)info[2], (int)info[3]);
     return BLASST_ERR_INVALID_ARG;
   }
   if (code == blasst::kBadPageId) {
@@ -223,20 +233,21 @@ cudaError_t launch_split(const blasst::DecodeArgs& a, long long grid,
 
 // The warp-MMA decode (decode_mma.cuh) for the sequential rule on a
 // contiguous cache with G <= 8, then the merge as for launch_decode.
-template <int G, int D, bool PAGED, int BATCH = 1>
+template <int G, int D, bool PAGED, int BATCH = 1, bool SEL = false>
 cudaError_t launch_mma_split(const blasst::DecodeMmaArgs& a, long long grid,
                              cudaStream_t st) {
   using C = blasst::DecodeMmaCfg;
   cudaError_t e = cudaFuncSetAttribute(
-      blasst::decode_mma_kernel<G, D, PAGED, BATCH>,
+      blasst::decode_mma_kernel<G, D, PAGED, BATCH, SEL>,
       cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_ALLOC);
   if (e != cudaSuccess) return e;
-  blasst::decode_mma_kernel<G, D, PAGED, BATCH>
+  blasst::decode_mma_kernel<G, D, PAGED, BATCH, SEL>
       <<<(unsigned)grid, blasst::kDecThreads, C::SMEM_ALLOC, st>>>(a);
   return cudaGetLastError();
 }
 
-// paged: the pool form; batch 2: the batched decision rule (contiguous)
+// paged: the pool form (over a.sel's blocks when set); batch 2: the batched
+// decision rule (contiguous)
 blasst_status_t launch_decode_mma(const blasst::DecodeMmaArgs& a, int G,
                                   int d, bool paged, long long grid,
                                   bool stats_only, void* o, float* lse,
@@ -245,7 +256,8 @@ blasst_status_t launch_decode_mma(const blasst::DecodeMmaArgs& a, int G,
   switch (G * 1000 + d) {
 #define BLASST_LAUNCH_MMA(GG, DD)                                           \
   case GG * 1000 + DD:                                                      \
-    e = paged ? launch_mma_split<GG, DD, true>(a, grid, st)                 \
+    e = a.sel   ? launch_mma_split<GG, DD, true, 1, true>(a, grid, st)      \
+        : paged ? launch_mma_split<GG, DD, true>(a, grid, st)               \
               : (batch == 2 ? launch_mma_split<GG, DD, false, 2>(a, grid, st) \
                             : launch_mma_split<GG, DD, false>(a, grid, st)); \
     break;
@@ -340,6 +352,22 @@ blasst_status_t carve_workspace(void* workspace, size_t workspace_bytes,
     *order = reinterpret_cast<int*>(static_cast<char*>(workspace) + o_bytes +
                                     l_bytes);
   return BLASST_OK;
+}
+
+// The two pool maps of the warp-MMA kernel (whole rows at d 128, see
+// decode_mma.cuh).
+bool encode_pool_maps(blasst::DecodeMmaArgs* m, const void* k_pages,
+                      const void* v_pages, int d, int page_size, int Hkv,
+                      int num_pages, long long page_stride, int box_rows) {
+  return d == 128
+             ? blasst::encode_pool_map_rows(&m->tk, k_pages, page_size, Hkv,
+                                            num_pages, page_stride, box_rows) &&
+                   blasst::encode_pool_map_rows(&m->tv, v_pages, page_size, Hkv,
+                                                num_pages, page_stride, box_rows)
+             : blasst::encode_pool_map(&m->tk, k_pages, d, page_size, Hkv,
+                                       num_pages, page_stride, box_rows) &&
+                   blasst::encode_pool_map(&m->tv, v_pages, d, page_size, Hkv,
+                                           num_pages, page_stride, box_rows);
 }
 
 // Paged calls whose grid is more than one wave decode the longest sequences
@@ -636,17 +664,8 @@ blasst_status_t blasst_decode_paged(const void* q, const void* k_pages,
     }
     const int box_rows = page_size < 64 ? page_size : 64;
     // d 128: whole rows per copy (5-D map); d 64: one 64-column box
-    const bool maps_ok =
-        d == 128
-            ? blasst::encode_pool_map_rows(&m.tk, k_pages, page_size, Hkv,
-                                           num_pages, page_stride, box_rows) &&
-                  blasst::encode_pool_map_rows(&m.tv, v_pages, page_size, Hkv,
-                                               num_pages, page_stride, box_rows)
-            : blasst::encode_pool_map(&m.tk, k_pages, d, page_size, Hkv,
-                                      num_pages, page_stride, box_rows) &&
-                  blasst::encode_pool_map(&m.tv, v_pages, d, page_size, Hkv,
-                                          num_pages, page_stride, box_rows);
-    if (!maps_ok)
+    if (!encode_pool_maps(&m, k_pages, v_pages, d, page_size, Hkv, num_pages,
+                          page_stride, box_rows))
       return cuda_status(cudaErrorInvalidValue, "paged decode tensor maps");
     m.q = static_cast<const __nv_bfloat16*>(q);
     m.counters = skip_stats ? skip_stats->counters : nullptr;
@@ -1147,6 +1166,375 @@ double blasst_fit_a(int n, const double* lambdas, const int* lengths) {
   double acc = 0.0;
   for (int i = 0; i < n; ++i) acc += std::log(lambdas[i] * (double)lengths[i]);
   return std::exp(acc / n);
+}
+
+// ---------------------------------------------------------------------------
+// Block-selected attention
+// ---------------------------------------------------------------------------
+namespace {
+// log2 of a page size the paged calls take, else -1
+int log2_page_size(int page_size) {
+  for (int l2 = 4; l2 <= 8; ++l2)
+    if (page_size == (1 << l2)) return l2;
+  return -1;
+}
+
+bool select_dim_ok(int d) { return d == 64 || d == 128; }
+
+// Heads per KV head of the packed query tiles: powers of two whose 128 / G
+// tokens fill whole 16-byte rows of the backward's lse and D boxes.
+bool select_group_ok(int G) { return G >= 1 && G <= 32 && (G & (G - 1)) == 0; }
+
+bool select_slots_ok(int n_sel, int n_first, int n_local) {
+  return n_sel >= 1 && n_first >= 0 && n_local >= 0 &&
+         (long long)n_first + n_local <= n_sel;
+}
+}  // namespace
+
+blasst_status_t blasst_block_means(const void* k, void* means, int B, int Hkv,
+                                   int Lkv, int d, void* stream) {
+  if (!k || !means) return BLASST_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1 || Lkv < 1) return BLASST_ERR_INVALID_ARG;
+  if (!select_dim_ok(d)) return BLASST_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(k) || !aligned16(means)) return BLASST_ERR_MISALIGNED;
+  blasst::MeansArgs a;
+  memset(&a, 0, sizeof a);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.means = static_cast<__nv_bfloat16*>(means);
+  a.Hkv = Hkv;
+  a.L = Lkv;
+  a.nblk = (int)(((long long)Lkv + blasst::kSelBlock - 1) / blasst::kSelBlock);
+  a.max_blocks = a.nblk;
+  const long long grid = (long long)B * Hkv * a.nblk;
+  if (grid > 0x7fffffffLL) return BLASST_ERR_UNSUPPORTED_SHAPE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d == 128)
+    blasst::block_means_kernel<128, false><<<(unsigned)grid, 128, 0, st>>>(a);
+  else
+    blasst::block_means_kernel<64, false><<<(unsigned)grid, 128, 0, st>>>(a);
+  return cuda_status(cudaGetLastError(), "block means launch");
+}
+
+blasst_status_t blasst_block_means_paged(
+    const void* k_pages, long long page_stride, int num_pages, int page_size,
+    const int* block_table, int max_pages, const int* seq_lens,
+    int max_seq_len, int n_new, void* means, int max_blocks, int B, int Hkv,
+    int d, void* stream) {
+  if (!k_pages || !block_table || !seq_lens || !means)
+    return BLASST_ERR_INVALID_ARG;
+  if (B < 1 || Hkv < 1 || num_pages < 1 || max_pages < 1 || max_seq_len < 1 ||
+      n_new < 0 || max_blocks < 1)
+    return BLASST_ERR_INVALID_ARG;
+  const int log2_page = log2_page_size(page_size);
+  if (log2_page < 0 || !select_dim_ok(d)) return BLASST_ERR_UNSUPPORTED_SHAPE;
+  const long long nblk =
+      ((long long)max_seq_len + blasst::kSelBlock - 1) / blasst::kSelBlock;
+  if ((long long)max_seq_len > (long long)max_pages * page_size ||
+      nblk > max_blocks)
+    return BLASST_ERR_INVALID_ARG;
+  if (page_stride < (long long)Hkv * page_size * d || page_stride % 8 != 0)
+    return BLASST_ERR_INVALID_ARG;
+  if (!aligned16(k_pages) || !aligned16(means)) return BLASST_ERR_MISALIGNED;
+  blasst::MeansArgs a;
+  memset(&a, 0, sizeof a);
+  a.k = static_cast<const __nv_bfloat16*>(k_pages);
+  a.means = static_cast<__nv_bfloat16*>(means);
+  a.Hkv = Hkv;
+  a.L = max_seq_len;
+  a.nblk = (int)nblk;
+  a.max_blocks = max_blocks;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.page_stride = page_stride;
+  a.log2_page = log2_page;
+  a.max_pages = max_pages;
+  a.num_pages = num_pages;
+  a.n_new = n_new;
+  // blocks the last n_new tokens can touch, wherever they start
+  long long ny = nblk;
+  if (n_new > 0 && ((long long)n_new + 62) / 64 + 1 < ny)
+    ny = ((long long)n_new + 62) / 64 + 1;
+  const long long nx = (long long)B * Hkv;
+  if (nx > 0x7fffffffLL || ny > 65535) return BLASST_ERR_UNSUPPORTED_SHAPE;
+  const dim3 grid((unsigned)nx, (unsigned)ny);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (d == 128)
+    blasst::block_means_kernel<128, true><<<grid, 128, 0, st>>>(a);
+  else
+    blasst::block_means_kernel<64, true><<<grid, 128, 0, st>>>(a);
+  return cuda_status(cudaGetLastError(), "block means launch");
+}
+
+blasst_status_t blasst_block_select(const void* q, const void* means, int* sel,
+                                    int B, int Hq, int Hkv, int Lq, int Lkv,
+                                    int d, int causal, int n_sel, int n_first,
+                                    int n_local, void* stream) {
+  if (!q || !means || !sel) return BLASST_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || Lkv < 1 || Hq % Hkv != 0)
+    return BLASST_ERR_INVALID_ARG;
+  if (!select_slots_ok(n_sel, n_first, n_local)) return BLASST_ERR_INVALID_ARG;
+  if (causal && (Lq > Lkv || n_local < 1)) return BLASST_ERR_INVALID_ARG;
+  if (!select_dim_ok(d) || Hq / Hkv > 32 || Lkv > 131072 || n_sel > 4096)
+    return BLASST_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(q) || !aligned16(means)) return BLASST_ERR_MISALIGNED;
+  blasst::SelectArgs a;
+  memset(&a, 0, sizeof a);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.means = static_cast<const __nv_bfloat16*>(means);
+  a.sel = sel;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.Lq = Lq;
+  a.Lkv = Lkv;
+  a.nblk = (Lkv + blasst::kSelBlock - 1) / blasst::kSelBlock;
+  a.causal = causal ? 1 : 0;
+  a.n_sel = n_sel;
+  a.n_first = n_first;
+  a.n_local = n_local;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(d == 128 ? blasst::launch_block_select<128>(a, B, st)
+                              : blasst::launch_block_select<64>(a, B, st),
+                     "block select launch");
+}
+
+blasst_status_t blasst_block_select_decode(const void* q, const void* means,
+                                           const int* seq_lens,
+                                           int max_seq_len, int max_blocks,
+                                           int* sel, int B, int Hq, int Hkv,
+                                           int d, int n_sel, int n_first,
+                                           int n_local, void* stream) {
+  if (!q || !means || !seq_lens || !sel) return BLASST_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hkv < 1 || max_seq_len < 1 || max_blocks < 1 ||
+      Hq % Hkv != 0)
+    return BLASST_ERR_INVALID_ARG;
+  if (!select_slots_ok(n_sel, n_first, n_local)) return BLASST_ERR_INVALID_ARG;
+  const long long nblk =
+      ((long long)max_seq_len + blasst::kSelBlock - 1) / blasst::kSelBlock;
+  if (nblk > max_blocks) return BLASST_ERR_INVALID_ARG;
+  if (!select_dim_ok(d) || Hq / Hkv > 32 || nblk > 16384 || n_sel > 4096 ||
+      (long long)B * Hkv > 0x7fffffffLL)
+    return BLASST_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(q) || !aligned16(means)) return BLASST_ERR_MISALIGNED;
+  blasst::SelectArgs a;
+  memset(&a, 0, sizeof a);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.means = static_cast<const __nv_bfloat16*>(means);
+  a.sel = sel;
+  a.seq_lens = seq_lens;
+  a.Hkv = Hkv;
+  a.G = Hq / Hkv;
+  a.Lq = 1;
+  a.Lkv = max_seq_len;
+  a.nblk = max_blocks;
+  a.n_sel = n_sel;
+  a.n_first = n_first;
+  a.n_local = n_local;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(
+      d == 128 ? blasst::launch_block_select_decode<128>(a, B, (int)nblk, st)
+               : blasst::launch_block_select_decode<64>(a, B, (int)nblk, st),
+      "block select launch");
+}
+
+size_t blasst_select_prefill_workspace_size(int B, int Hq, int Hkv, int Lq,
+                                            int Lkv) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || Lkv < 1 || Hq % Hkv != 0 ||
+      !select_group_ok(Hq / Hkv))
+    return 0;
+  return blasst::sel_workspace(B, Hq, Hkv, Lq, Lkv).total;
+}
+
+size_t blasst_select_prefill_backward_workspace_size(int B, int Hq, int Hkv,
+                                                     int Lq, int Lkv, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || Lkv < 1 || Hq % Hkv != 0 ||
+      !select_group_ok(Hq / Hkv) || d != blasst::kBwdD)
+    return 0;
+  return blasst::sel_bwd_workspace(B, Hq, Hkv, Lq, Lkv).total;
+}
+
+namespace {
+// Checks shared by the selected forward and backward.
+blasst_status_t check_select_prefill(int B, int Hq, int Hkv, int Lq, int Lkv,
+                                     int n_sel, float scale, int causal) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Lq < 1 || Lkv < 1 || Hq % Hkv != 0 ||
+      n_sel < 1)
+    return BLASST_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return BLASST_ERR_INVALID_ARG;
+  if (causal && Lq > Lkv) return BLASST_ERR_INVALID_ARG;
+  if (!select_group_ok(Hq / Hkv) || n_sel > blasst::kSelMaxBlocks ||
+      Lkv > blasst::kSelMaxBlocks * blasst::kSelBlock ||
+      Lq > 0x7fffffff / blasst::kSelMaxBlocks ||
+      (long long)B * Hq > 0x7fffffffLL)
+    return BLASST_ERR_UNSUPPORTED_SHAPE;
+  return BLASST_OK;
+}
+}  // namespace
+
+blasst_status_t blasst_select_prefill(const void* q, const void* k,
+                                      const void* v, const int* sel, void* o,
+                                      float* lse, int B, int Hq, int Hkv,
+                                      int Lq, int Lkv, int d, int n_sel,
+                                      float scale, int causal, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  if (!q || !k || !v || !sel || !o) return BLASST_ERR_INVALID_ARG;
+  const blasst_status_t rc =
+      check_select_prefill(B, Hq, Hkv, Lq, Lkv, n_sel, scale, causal);
+  if (rc != BLASST_OK) return rc;
+  if (!select_dim_ok(d)) return BLASST_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o))
+    return BLASST_ERR_MISALIGNED;
+  if (!workspace ||
+      workspace_bytes < blasst::sel_workspace(B, Hq, Hkv, Lq, Lkv).total)
+    return BLASST_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return BLASST_ERR_MISALIGNED;
+  blasst::SelProblem p;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.sel = sel;
+  p.o = o;
+  p.lse = lse;
+  p.workspace = workspace;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.Lq = Lq;
+  p.Lkv = Lkv;
+  p.d = d;
+  p.n_sel = n_sel;
+  p.causal = causal ? 1 : 0;
+  p.scale = scale;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(d == 128 ? blasst::launch_select_prefill<128>(p, st)
+                              : blasst::launch_select_prefill<64>(p, st),
+                     "selected prefill launch");
+}
+
+blasst_status_t blasst_select_prefill_backward(
+    const void* q, const void* k, const void* v, const void* o,
+    const void* dout, const float* lse, const int* sel, void* dq, void* dk,
+    void* dv, int B, int Hq, int Hkv, int Lq, int Lkv, int d, int n_sel,
+    float scale, int causal, void* workspace, size_t workspace_bytes,
+    void* stream) {
+  if (!q || !k || !v || !o || !dout || !lse || !sel || !dq || !dk || !dv)
+    return BLASST_ERR_INVALID_ARG;
+  const blasst_status_t rc =
+      check_select_prefill(B, Hq, Hkv, Lq, Lkv, n_sel, scale, causal);
+  if (rc != BLASST_OK) return rc;
+  if (d != blasst::kBwdD) return BLASST_ERR_UNSUPPORTED_SHAPE;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
+      !aligned16(dout) || !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return BLASST_ERR_MISALIGNED;
+  if (!workspace ||
+      workspace_bytes < blasst::sel_bwd_workspace(B, Hq, Hkv, Lq, Lkv).total)
+    return BLASST_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return BLASST_ERR_MISALIGNED;
+  blasst::SelBwdProblem p;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.o = o;
+  p.dout = dout;
+  p.lse = lse;
+  p.sel = sel;
+  p.dq = dq;
+  p.dk = dk;
+  p.dv = dv;
+  p.workspace = workspace;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.Lq = Lq;
+  p.Lkv = Lkv;
+  p.n_sel = n_sel;
+  p.causal = causal ? 1 : 0;
+  p.scale = scale;
+  return cuda_status(
+      blasst::launch_select_backward(p, static_cast<cudaStream_t>(stream)),
+      "selected backward launch");
+}
+
+int blasst_select_decode_splits(int B, int Hq, int Hkv, int n_sel) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || n_sel < 1 || Hq % Hkv != 0) return 1;
+  const int G = Hq / Hkv;
+  const long long units = (long long)B * Hkv * (G > 8 ? G / 8 : 1);
+  // the waves of 3 CTAs per SM times one item's blocks and its fixed cost
+  // (the list, q, its partial and merge row: about 3 blocks' time)
+  const long long slots = (long long)kNumSmB200 * 3;
+  long long best = 1;
+  double best_t = 0.0;
+  for (long long s = 1; s <= n_sel; ++s) {
+    const double waves = std::ceil((double)(units * s) / (double)slots);
+    const double t = waves * (std::ceil((double)n_sel / (double)s) + 3.0);
+    if (s == 1 || t < best_t - 1e-9) {
+      best_t = t;
+      best = s;
+    }
+  }
+  return (int)best;
+}
+
+blasst_status_t blasst_select_decode_paged(
+    const void* q, const void* k_pages, const void* v_pages,
+    long long page_stride, int num_pages, int page_size,
+    const int* block_table, int max_pages, const int* seq_lens,
+    int max_seq_len, const int* sel, int n_sel, void* o, float* lse, int B,
+    int Hq, int Hkv, int d, float scale, int num_splits, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !sel || !o)
+    return BLASST_ERR_INVALID_ARG;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || num_pages < 1 ||
+      max_pages < 1 || max_seq_len < 1 || num_splits < 0 || n_sel < 1)
+    return BLASST_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return BLASST_ERR_INVALID_ARG;
+  const int log2_page = log2_page_size(page_size);
+  if (log2_page < 0) return BLASST_ERR_UNSUPPORTED_SHAPE;
+  if ((long long)max_seq_len > (long long)max_pages * page_size)
+    return BLASST_ERR_INVALID_ARG;
+  const int Gq = Hq / Hkv;
+  if (!select_dim_ok(d) || !decode_group_ok(Gq) ||
+      n_sel > blasst::kSelDecodeMax || max_seq_len > 0x7fffffff - 64)
+    return BLASST_ERR_UNSUPPORTED_SHAPE;
+  const int G = Gq > 8 ? 8 : Gq;
+  const int kv_div = Gq / G;  // tiles of G heads per KV head
+  if (page_stride < (long long)Hkv * page_size * d || page_stride % 8 != 0)
+    return BLASST_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      !aligned16(o))
+    return BLASST_ERR_MISALIGNED;
+  const int S = num_splits == 0 ? blasst_select_decode_splits(B, Hq, Hkv, n_sel)
+                                : num_splits;
+  if (S > n_sel) return BLASST_ERR_INVALID_ARG;
+  const long long grid = (long long)B * Hkv * kv_div * S;
+  if (grid > 0x7fffffffLL || (long long)B * Hq > 0x7fffffffLL)
+    return BLASST_ERR_UNSUPPORTED_SHAPE;
+  blasst::DecodeMmaArgs m;
+  memset(&m, 0, sizeof m);
+  const blasst_status_t ws = carve_workspace(workspace, workspace_bytes, B, Hq,
+                                             d, S, &m.o_part, &m.lse_part);
+  if (ws != BLASST_OK) return ws;
+  if (!encode_pool_maps(&m, k_pages, v_pages, d, page_size, Hkv, num_pages,
+                        page_stride, page_size < 64 ? page_size : 64))
+    return cuda_status(cudaErrorInvalidValue, "selected decode tensor maps");
+  m.q = static_cast<const __nv_bfloat16*>(q);
+  m.Hkv = Hkv;
+  m.Lkv = max_seq_len;
+  m.nk = (max_seq_len + blasst::kDecBc - 1) / blasst::kDecBc;
+  m.S = S;
+  m.scale = scale;
+  m.ln_lambda = -INFINITY;  // dense over the selected blocks
+  m.block_table = block_table;
+  m.seq_lens = seq_lens;
+  m.max_pages = max_pages;
+  m.num_pages = num_pages;
+  m.log2_page = log2_page;
+  m.sel = sel;
+  m.n_sel = n_sel;
+  m.kv_div = kv_div;
+  return launch_decode_mma(m, G, d, true, grid, false, o, lse, B * Hq,
+                           static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,823 @@
+// block_select.cuh -- the cheap score of block-selected attention: key-block
+// means, and the selection of the best-scoring blocks per query.
+//
+//   c_j = mean of the keys of block j (64 tokens, the last one ragged), bf16
+//   s_rj = sum over the G query heads of a KV head of q_gr . c_j
+//        = (sum_g q_gr) . c_j
+//
+// Row r takes the first n_first and the last n_local of its visible blocks,
+// and fills the rest of its n_sel slots with the best scores among the other
+// visible blocks, equal scores to the lower index.  The list is written in
+// ascending order, -1 in slots left over.
+//
+// The chosen set is the one the exact scores give.  Scores are first formed
+// in float32 (tensor core in the prompt form) together with a bound e on
+// their error; blocks within 2 e of the cut are scored again in float64 and
+// ranked by that (a few per cent of the rows have any).
+#pragma once
+
+#include "decode_mma.cuh"
+
+namespace blasst {
+
+constexpr int kSelBlock = 64;  // keys per selection block
+
+// ---------------------------------------------------------------------------
+// Block means
+// ---------------------------------------------------------------------------
+struct MeansArgs {
+  const __nv_bfloat16* k;  // [B, Hkv, L, d], or the pool
+  __nv_bfloat16* means;    // [B, Hkv, max_blocks, d]
+  int Hkv, L, nblk;        // L: keys (contiguous), upper bound (paged)
+  int max_blocks;          // blocks per (sequence, head) in means
+  // paged
+  const int* block_table;
+  const int* seq_lens;
+  long long page_stride;
+  int log2_page, max_pages, num_pages, n_new;
+};
+
+// One CTA of 128 threads per block: a thread sums 8 columns (16 bytes) of
+// every (128 / (D/8))-th row, all its loads in flight at once; the row groups
+// are added through a shuffle and shared memory in a fixed order.  Bound by
+// HBM: the keys are read once.
+template <int D, bool PAGED>
+__global__ void __launch_bounds__(128) block_means_kernel(const MeansArgs a) {
+  constexpr int CH = D / 8;        // 16-byte chunks of a row
+  constexpr int RG = 128 / CH;     // row groups
+  constexpr int NR = kSelBlock / RG;
+  __shared__ float red[4][D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int chunk = tid % CH, rg = tid / CH;
+  const int bh = PAGED ? (int)blockIdx.x : (int)(blockIdx.x / a.nblk);
+  const int b = bh / a.Hkv, h = bh - b * a.Hkv;
+  int L = a.L, j;
+  const int* bt = nullptr;
+  if constexpr (PAGED) {
+    L = __ldg(a.seq_lens + b);
+    if (L < 0 || L > a.L) {  // uniform across the CTA
+      if (tid == 0) record_error(kBadSeqLen, (unsigned)b, (unsigned)L, 0);
+      return;
+    }
+    // the blocks the last n_new tokens lie in (all of them for 0)
+    const int first = a.n_new > 0 && a.n_new < L ? L - a.n_new : 0;
+    const long long jl = first / kSelBlock + (long long)blockIdx.y;
+    if (jl * kSelBlock >= L) return;
+    j = (int)jl;
+    bt = a.block_table + (size_t)b * a.max_pages;
+  } else {
+    j = (int)(blockIdx.x - (unsigned)bh * (unsigned)a.nblk);
+  }
+  const int t0 = j * kSelBlock;
+  const int n = min(kSelBlock, L - t0);
+  uint4 w[NR];
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int row = i * RG + rg;
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (row < n) {
+      const __nv_bfloat16* src;
+      if constexpr (PAGED) {
+        const int t = t0 + row;
+        const int id = __ldg(bt + (t >> a.log2_page));
+        if (id < 0 || id >= a.num_pages) {
+          record_error(kBadPageId, (unsigned)b, (unsigned)(t >> a.log2_page),
+                       (unsigned)id);
+          bad = true;
+          continue;
+        }
+        const int ps = 1 << a.log2_page;
+        src = a.k + (long long)id * a.page_stride +
+              ((long long)h * ps + (t & (ps - 1))) * D;
+      } else {
+        src = a.k + ((size_t)bh * a.L + t0 + row) * D;
+      }
+      w[i] = __ldg(reinterpret_cast<const uint4*>(src) + chunk);
+    }
+  }
+  if constexpr (PAGED) {
+    if (__syncthreads_or(bad)) return;  // the block's mean stays as it was
+  }
+  float s[8];
+#pragma unroll
+  for (int x = 0; x < 8; ++x) s[x] = 0.f;
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      s[2 * x] += bf16lo(u[x]);
+      s[2 * x + 1] += bf16hi(u[x]);
+    }
+  }
+#pragma unroll
+  for (int o = CH; o < 32; o <<= 1)  // lanes of the warp on the same chunk
+#pragma unroll
+    for (int x = 0; x < 8; ++x) s[x] += __shfl_xor_sync(0xffffffffu, s[x], o);
+  if (lane < CH) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) red[warp][chunk * 8 + x] = s[x];
+  }
+  __syncthreads();
+  if (tid < D / 2) {
+    const float fn = (float)n;
+    float m[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int c = 2 * tid + e;
+      m[e] = ((red[0][c] + red[1][c]) + (red[2][c] + red[3][c])) / fn;
+    }
+    reinterpret_cast<uint32_t*>(a.means + ((size_t)bh * a.max_blocks + j) *
+                                              D)[tid] = pack_bf16x2(m[0], m[1]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Selection among the scores of one row
+// ---------------------------------------------------------------------------
+// The threads that work on one row: a warp, or a whole CTA.
+struct WarpGroup {
+  static constexpr int kThreads = 32;
+  int id, warp, nwarps;
+  __device__ WarpGroup() : id(threadIdx.x & 31), warp(0), nwarps(1) {}
+  __device__ void sync() { __syncwarp(); }
+  __device__ int add(int x) { return (int)__reduce_add_sync(~0u, (unsigned)x); }
+  __device__ float max(float x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+    return x;
+  }
+  // exclusive rank of the set flags, and their number
+  __device__ int rank(bool f, int& total) {
+    const unsigned m = __ballot_sync(~0u, f);
+    total = __popc(m);
+    return __popc(m & ((1u << id) - 1u));
+  }
+};
+
+template <int NT>
+struct CtaGroup {
+  static constexpr int kThreads = NT;
+  static constexpr int kWarps = NT / 32;
+  int id, warp, nwarps, flip;
+  uint32_t* scratch;  // [2][kWarps] shared
+  __device__ explicit CtaGroup(uint32_t* s)
+      : id(threadIdx.x), warp(threadIdx.x >> 5), nwarps(kWarps), flip(0),
+        scratch(s) {}
+  __device__ void sync() { __syncthreads(); }
+  // Each reduction writes its own half of the scratch words, alternating, so
+  // one barrier per reduction separates readers from the next writers.
+  __device__ const uint32_t* share(uint32_t x) {
+    uint32_t* s = scratch + flip * kWarps;
+    flip ^= 1;
+    if ((id & 31) == 0) s[warp] = x;
+    __syncthreads();
+    return s;
+  }
+  __device__ int add(int x) {
+    const uint32_t* s = share(__reduce_add_sync(~0u, (unsigned)x));
+    int t = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) t += (int)s[w];
+    return t;
+  }
+  __device__ float max(float x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+    const uint32_t* s = share(__float_as_uint(x));
+    float t = __uint_as_float(s[0]);
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) t = fmaxf(t, __uint_as_float(s[w]));
+    return t;
+  }
+  __device__ int rank(bool f, int& total) {
+    const unsigned m = __ballot_sync(~0u, f);
+    const uint32_t* s = share(__popc(m));
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += (int)s[w];
+      total += (int)s[w];
+    }
+    return before + __popc(m & ((1u << (id & 31)) - 1u));
+  }
+};
+
+// Cut of the k largest of s[0..n): every s > v is in, and of those equal to
+// v the lowest indices fill up; a is the smallest value taken, b the largest
+// left (a == b when equal values straddle the cut).  1 <= k < n; s holds no
+// NaN.  Bisection on the value between the extremes, ended early by a
+// midpoint that separates exactly k.
+struct Cut {
+  float v, a, b;
+};
+template <class GroupT>
+__device__ Cut find_cut(GroupT& g, const float* s, int n, int k) {
+  float mx = -INFINITY, mn = INFINITY;  // of the finite values
+  int n_hi = 0, n_fin = 0;
+  for (int i = g.id; i < n; i += GroupT::kThreads) {
+    const float x = s[i];
+    if (x == INFINITY) ++n_hi;
+    if (fabsf(x) < INFINITY) {
+      ++n_fin;
+      mx = fmaxf(mx, x);
+      mn = fminf(mn, x);
+    }
+  }
+  n_hi = g.add(n_hi);
+  n_fin = g.add(n_fin);
+  mx = g.max(mx);
+  mn = -g.max(-mn);
+  if (n_hi > k) return {INFINITY, INFINITY, INFINITY};
+  if (n_hi + n_fin < k) return {-INFINITY, -INFINITY, -INFINITY};
+  // in [lo, hi): at least k values are >= lo, fewer than k are >= hi
+  float t;  // a threshold that exactly k values reach
+  bool exact = false;
+  if (n_hi == k) {
+    t = INFINITY;
+    exact = true;
+  } else {
+    float lo = mn, hi = INFINITY;
+    int c = n_hi + n_fin;
+    t = mn;
+    if (c == k) exact = true;
+    bool first = true;
+    while (!exact) {
+      float mid;
+      if (first) {
+        mid = mx;
+        first = false;
+        if (!(mid > lo)) break;  // all finite values equal
+      } else {
+        mid = 0.5f * lo + 0.5f * hi;
+        if (!(mid > lo && mid < hi)) break;
+      }
+      c = 0;
+      for (int i = g.id; i < n; i += GroupT::kThreads) c += s[i] >= mid;
+      c = g.add(c);
+      if (c == k) {
+        t = mid;
+        exact = true;
+      } else if (c > k) {
+        lo = mid;
+        if (mid == mx) break;  // more than k values equal the largest
+      } else {
+        hi = mid;
+      }
+    }
+    if (!exact) return {lo, lo, lo};
+  }
+  float a = INFINITY, b = -INFINITY;
+  for (int i = g.id; i < n; i += GroupT::kThreads) {
+    const float x = s[i];
+    if (x >= t) a = fminf(a, x);
+    else b = fmaxf(b, x);
+  }
+  a = -g.max(-a);
+  b = g.max(b);
+  return {a, a, b};
+}
+
+// Writes the row's n_sel slots: blocks [0, f), the best k of the candidates
+// [f, m1) whose approximate scores s[0 .. m1 - f) are off by at most eps
+// each, and [m1, end).  exact(j) (taken by a whole warp) is the float64
+// score of block j.  s is overwritten where the cut needs it.
+template <class GroupT, class ExactT>
+__device__ void select_row(GroupT& g, float* s, int f, int m1, int end, int k,
+                           int n_sel, float eps, int* out, ExactT exact) {
+  const int n = m1 - f;
+  const int lane = threadIdx.x & 31;
+  int at = f;  // slots written so far
+  for (int i = g.id; i < f; i += GroupT::kThreads) out[i] = i;
+  if (k >= n) {
+    for (int i = g.id; i < n; i += GroupT::kThreads) out[at + i] = f + i;
+    at += n;
+  } else if (k > 0) {
+    Cut c;
+    bool again = !(eps < INFINITY);  // a bound that overflowed: all exact
+    if (again) {
+      c = {0.f, -INFINITY, INFINITY};
+    } else {
+      c = find_cut(g, s, n, k);
+      // the scores are exact when eps is 0; otherwise the order is certain
+      // only when the cut is wider than the two errors
+      again = eps > 0.f && !(c.a - c.b > 2.f * eps);
+    }
+    if (again) {
+      // above b + 2 eps: better than every value left out; below a - 2 eps:
+      // worse than all k taken; between: the distance of the exact score to
+      // the cut, whose rounding to float32 is relative to that distance
+      const float up = c.b + 2.f * eps, dn = c.a - 2.f * eps;
+      const bool all = !(eps < INFINITY);
+      g.sync();
+      for (int i = g.warp; i < n; i += g.nwarps) {
+        const float x = s[i];
+        float y;
+        if (!all && x > up) {
+          y = INFINITY;
+        } else if (!all && x < dn) {
+          y = -INFINITY;
+        } else {
+          const double e = exact(f + i) - (double)c.v;
+          // (a non-finite difference of a huge score: its own infinity)
+          y = isnan(e) ? -INFINITY : (float)e;
+        }
+        __syncwarp();
+        if (lane == 0) s[i] = y;
+      }
+      g.sync();
+      c = find_cut(g, s, n, k);
+    }
+    // values above the cut, then equal ones in ascending index
+    int left = k;
+    {
+      int above = 0;
+      for (int i = g.id; i < n; i += GroupT::kThreads) above += s[i] > c.v;
+      left -= g.add(above);
+    }
+    for (int i0 = 0; i0 < n; i0 += GroupT::kThreads) {
+      const int i = i0 + g.id;
+      const float x = i < n ? s[i] : -INFINITY;
+      int total;
+      const bool eq = i < n && x == c.v;
+      const int er = g.rank(eq, total);
+      const bool take = i < n && (x > c.v || (eq && er < left));
+      left -= min(left, total);
+      const int r = g.rank(take, total);
+      if (take) out[at + r] = f + i;
+      at += total;
+    }
+  }
+  for (int i = m1 + g.id; i < end; i += GroupT::kThreads) out[at + i - m1] = i;
+  at += end - m1;
+  for (int i = at + g.id; i < n_sel; i += GroupT::kThreads) out[i] = -1;
+}
+
+struct SelectArgs {
+  const __nv_bfloat16* q;      // [B, Hq, Lq, d]; decode [B, Hq, d]
+  const __nv_bfloat16* means;  // [B, Hkv, nblk, d]
+  int* sel;                    // [B, Hkv, Lq, n_sel]; decode [B, Hkv, n_sel]
+  const int* seq_lens;         // decode
+  int Hkv, G, Lq, Lkv, nblk;   // Lkv: upper bound on seq_lens in decode
+  int causal, n_sel, n_first, n_local;
+  int ntile, ld;               // prompt: row tiles, score row stride (floats)
+};
+
+// The row's regions: [0, f) and [m1, end) always taken, k of [f, m1) by score.
+struct SelRange {
+  int f, m1, end, k;
+};
+__device__ __forceinline__ SelRange sel_range(int last, int n_sel, int n_first,
+                                              int n_local) {
+  SelRange r;
+  r.end = last + 1;
+  r.f = min(n_first, r.end);
+  r.m1 = max(r.f, r.end - n_local);
+  r.k = n_sel - r.f - (r.end - r.m1);
+  return r;
+}
+
+// Relative error bound of the float32 scores, against |sum_g |q_g|| |c|:
+// splitting the head sum into two bf16 parts loses 2^-18 of it, its float32
+// sum G 2^-24 <= 2^-19 (G <= 32), and the accumulation of d/8 + 16 partial
+// products at most 2^-23 each, 2^-18 for d = 128: together below 2^-16.
+constexpr float kSelEps = 1.52587890625e-05f;  // 2^-16
+// Norms are summed over values scaled by 2^40, so that squares of small
+// values stay above float32's smallest (a sum that overflows only sends the
+// row to the float64 scores).
+constexpr float kNormUp = 1099511627776.f, kNormDown = 1.f / 1099511627776.f;
+
+// The error bound of a row whose |sum_g |q_g|| is nq, against means of norm
+// at most nc.  The product is formed first: where it overflows, so may the
+// scores, and the bound has to be infinite.
+__device__ __forceinline__ float score_eps(float nq, float nc) {
+  const float e = kSelEps * (nq * nc);
+  return nq > 0.f && nc > 0.f ? fmaxf(e, 1e-37f) : e;
+}
+
+// The float64 score of one block for the whole warp; qd holds the lane's
+// D / 32 head sums.
+template <int D>
+__device__ __forceinline__ double exact_score(const double (&qd)[D / 32],
+                                              const __nv_bfloat16* c) {
+  const int lane = threadIdx.x & 31;
+  double e = 0.0;
+#pragma unroll
+  for (int x = 0; x < D / 32; ++x)
+    e += qd[x] * (double)__bfloat162float(c[lane + 32 * x]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) e += __shfl_xor_sync(~0u, e, o);
+  return e;
+}
+
+// ---------------------------------------------------------------------------
+// One token per sequence: a CTA per (sequence, KV head) scores every block
+// (float32 on the CUDA cores: one pass over the means, the bound is HBM) and
+// selects.
+// ---------------------------------------------------------------------------
+constexpr int kSelDecThreads = 512;
+
+template <int D>
+__global__ void __launch_bounds__(kSelDecThreads)
+    block_select_decode_kernel(const SelectArgs a) {
+  constexpr int CH = D / 8;           // lanes per block row
+  constexpr int RPW = 32 / CH;        // rows a warp reads at once
+  constexpr int NW = kSelDecThreads / 32;
+  constexpr int UN = 4;
+  extern __shared__ float sel_smem[];  // [nblk] scores
+  __shared__ float qs[D], qa[D];
+  __shared__ uint32_t scratch[2 * NW];
+  __shared__ uint32_t cmax_s;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int bh = blockIdx.x;
+  const int b = bh / a.Hkv, h = bh - b * a.Hkv;
+  const int L = __ldg(a.seq_lens + b);
+  int* out = a.sel + (size_t)bh * a.n_sel;
+  if (L < 0 || L > a.Lkv) {  // uniform across the CTA
+    if (tid == 0) record_error(kBadSeqLen, (unsigned)b, (unsigned)L, 0);
+    for (int i = tid; i < a.n_sel; i += kSelDecThreads) out[i] = -1;
+    return;
+  }
+  if (L == 0) {
+    for (int i = tid; i < a.n_sel; i += kSelDecThreads) out[i] = -1;
+    return;
+  }
+  const SelRange r = sel_range((L - 1) / kSelBlock, a.n_sel, a.n_first,
+                               a.n_local);
+  const __nv_bfloat16* q =
+      a.q + ((size_t)b * a.Hkv + h) * (size_t)a.G * D;  // G rows of D
+  if (tid == 0) cmax_s = 0u;
+  if (tid < D) {
+    float x = 0.f, y = 0.f;
+    for (int g = 0; g < a.G; ++g) {
+      const float z = __bfloat162float(q[(size_t)g * D + tid]);
+      x += z;
+      y += fabsf(z);
+    }
+    qs[tid] = x;
+    qa[tid] = y;
+  }
+  __syncthreads();
+  const int n = r.m1 - r.f;
+  const __nv_bfloat16* c0 = a.means + (size_t)bh * a.nblk * D;
+  if (r.k > 0 && r.k < n) {
+    const int chunk = lane % CH, rl = lane / CH;
+    float qr[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) qr[x] = qs[chunk * 8 + x];
+    float cm = 0.f;
+    for (int i0 = warp * RPW * UN; i0 < n; i0 += NW * RPW * UN) {
+      uint4 w[UN];
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const int i = i0 + u * RPW + rl;
+        w[u] = i < n ? __ldg(reinterpret_cast<const uint4*>(
+                                 c0 + (size_t)(r.f + i) * D) + chunk)
+                     : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const uint32_t ww[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        float dot = 0.f, nn = 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float lo = bf16lo(ww[x]), hi = bf16hi(ww[x]);
+          dot = fmaf(qr[2 * x], lo, dot);
+          dot = fmaf(qr[2 * x + 1], hi, dot);
+          nn = fmaf(lo * kNormUp, lo * kNormUp, nn);
+          nn = fmaf(hi * kNormUp, hi * kNormUp, nn);
+        }
+#pragma unroll
+        for (int o = CH / 2; o; o >>= 1) {
+          dot += __shfl_xor_sync(~0u, dot, o);
+          nn += __shfl_xor_sync(~0u, nn, o);
+        }
+        const int i = i0 + u * RPW + rl;
+        if (i < n && chunk == 0) {
+          sel_smem[i] = isnan(dot) ? -INFINITY : dot;
+        }
+        // (a NaN's bits compare above every number's)
+        cm = __uint_as_float(max(__float_as_uint(cm), __float_as_uint(fabsf(nn))));
+      }
+    }
+    const uint32_t cw = __reduce_max_sync(~0u, __float_as_uint(cm));
+    if (lane == 0) atomicMax(&cmax_s, cw);
+  }
+  __syncthreads();
+  CtaGroup<kSelDecThreads> g(scratch);
+  float eps = 0.f;
+  if (r.k > 0 && r.k < n) {
+    float qq = 0.f;
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x) {
+      const float y = qa[lane + 32 * x] * kNormUp;
+      qq = fmaf(y, y, qq);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) qq += __shfl_xor_sync(~0u, qq, o);
+    eps = score_eps(sqrtf(qq) * kNormDown,
+                    sqrtf(__uint_as_float(cmax_s)) * kNormDown);
+  }
+  double qd[D / 32];
+  bool have_q = false;
+  select_row(g, sel_smem, r.f, r.m1, r.end, r.k, a.n_sel, eps, out,
+             [&](int j) {
+               if (!have_q) {
+                 have_q = true;
+#pragma unroll
+                 for (int x = 0; x < D / 32; ++x) {
+                   qd[x] = 0.0;
+                   for (int gg = 0; gg < a.G; ++gg)
+                     qd[x] += (double)__bfloat162float(
+                         q[(size_t)gg * D + lane + 32 * x]);
+                 }
+               }
+               return exact_score<D>(qd, c0 + (size_t)j * D);
+             });
+}
+
+template <int D>
+cudaError_t launch_block_select_decode(const SelectArgs& a, int B, int nblk,
+                                       cudaStream_t st) {
+  const int smem = nblk * 4;
+  cudaError_t e = cudaFuncSetAttribute(
+      block_select_decode_kernel<D>,
+      cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  block_select_decode_kernel<D>
+      <<<(unsigned)(B * a.Hkv), kSelDecThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Every row of a prompt: a CTA of 8 warps takes TM rows of one KV head.  The
+// head sums are split into two bf16 parts (16 bits of each sum) and scored
+// against the means on the tensor core (mma.sync: 2 d deep, far from its
+// limit, and the scores land in registers, one shared-memory store away from
+// the selection); all scores of the TM rows stay in shared memory, then each
+// warp selects for its rows.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4],
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+      "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// 16-byte asynchronous copy; zeros when !valid (nothing is read then).
+__device__ __forceinline__ void cp_async_16(void* dst_smem, const void* src,
+                                            bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   smem_u32(dst_smem)),
+               "l"(src), "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_but_one() {
+  asm volatile("cp.async.wait_group 1;" ::: "memory");
+}
+
+template <int D, int TM>
+struct SelectCfg {
+  static constexpr int QROW = 2 * D * 2;  // hi and lo halves of a row, bytes
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_C = OFF_Q + TM * QROW;       // [2][64][D] bf16
+  static constexpr int CBYTES = kSelBlock * D * 2;
+  static constexpr int OFF_N = OFF_C + 2 * CBYTES;      // f32 [TM] |q| bound
+  static constexpr int OFF_CM = OFF_N + TM * 4;
+  static constexpr int OFF_S = (OFF_CM + 4 + 127) / 128 * 128;
+  static constexpr int smem(int ld) { return OFF_S + TM * ld * 4; }
+};
+
+template <int D, int TM>
+__global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
+  using C = SelectCfg<D, TM>;
+  constexpr int CH = D / 8;
+  constexpr int KST = D / 16;
+  constexpr int WM = TM / 16;       // warps along the rows
+  constexpr int WN = 8 / WM;        // warps along the blocks
+  constexpr int NT = kSelBlock / WN / 8;
+  extern __shared__ __align__(128) uint8_t sel_raw[];
+  uint8_t* sq = sel_raw + C::OFF_Q;
+  uint8_t* sc = sel_raw + C::OFF_C;
+  float* nrm = reinterpret_cast<float*>(sel_raw + C::OFF_N);
+  uint32_t* cmax_s = reinterpret_cast<uint32_t*>(sel_raw + C::OFF_CM);
+  float* S = reinterpret_cast<float*>(sel_raw + C::OFF_S);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nbh = gridDim.x / a.ntile;
+  const int tile = a.ntile - 1 - (int)(blockIdx.x / nbh);  // longest first
+  const int bh = blockIdx.x % nbh;
+  const int b = bh / a.Hkv, h = bh - b * a.Hkv;
+  const int row0 = tile * TM;
+  const int nrow = min(TM, a.Lq - row0);
+  const int off = a.causal ? a.Lkv - a.Lq : 0;
+  // blocks any row of the tile may score
+  const int key_end = a.causal ? row0 + nrow - 1 + off : a.Lkv - 1;
+  const int ncand = key_end / kSelBlock + 1 - a.n_local;
+  const int nct = ncand > 0 ? (ncand + kSelBlock - 1) / kSelBlock : 0;
+  const __nv_bfloat16* c0 = a.means + (size_t)bh * a.nblk * D;
+  if (tid == 0) *cmax_s = 0u;
+
+  auto load_c = [&](int ct) {
+    uint8_t* dst = sc + (ct & 1) * C::CBYTES;
+    for (int e = tid; e < kSelBlock * CH; e += 256) {
+      const int row = e / CH, ch = e % CH;
+      const int j = ct * kSelBlock + row;
+      const bool ok = j < a.nblk;
+      cp_async_16(dst + row * (D * 2) + ((ch ^ (row & 7)) << 4),
+                  c0 + (size_t)(ok ? j : 0) * D + ch * 8, ok);
+    }
+    cp_async_commit();
+  };
+  if (nct > 0) load_c(0);
+  // head sums of the TM rows: 8 columns per thread and row
+  {
+    const __nv_bfloat16* q0 =
+        a.q + ((size_t)b * a.Hkv + h) * (size_t)a.G * a.Lq * D;
+    for (int e = tid; e < TM * CH; e += 256) {
+      const int row = e / CH, ch = e % CH;
+      float x[8], y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = y[i] = 0.f;
+      if (row < nrow) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+                               q0 + (size_t)(row0 + row) * D) + ch;
+        const size_t hs = (size_t)a.Lq * CH;  // 16-byte chunks per head
+#pragma unroll 4
+        for (int g = 0; g < a.G; ++g) {
+          const uint4 w = __ldg(src + g * hs);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float lo = bf16lo(ww[i]), hi = bf16hi(ww[i]);
+            x[2 * i] += lo;
+            x[2 * i + 1] += hi;
+            y[2 * i] += fabsf(lo);
+            y[2 * i + 1] += fabsf(hi);
+          }
+        }
+      }
+      uint32_t ph[4], pl[4];
+      float nn = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ph[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+        pl[i] = pack_bf16x2(x[2 * i] - bf16lo(ph[i]),
+                            x[2 * i + 1] - bf16hi(ph[i]));
+        nn = fmaf(y[2 * i] * kNormUp, y[2 * i] * kNormUp, nn);
+        nn = fmaf(y[2 * i + 1] * kNormUp, y[2 * i + 1] * kNormUp, nn);
+      }
+      uint8_t* dst = sq + row * C::QROW;
+      *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) << 4)) =
+          make_uint4(ph[0], ph[1], ph[2], ph[3]);
+      *reinterpret_cast<uint4*>(dst + (((ch + CH) ^ (row & 7)) << 4)) =
+          make_uint4(pl[0], pl[1], pl[2], pl[3]);
+#pragma unroll
+      for (int o = CH / 2; o; o >>= 1) nn += __shfl_xor_sync(~0u, nn, o);
+      if (ch == 0) nrm[row] = sqrtf(nn) * kNormDown;
+    }
+  }
+  __syncthreads();
+  const int wm = warp % WM, wn = warp / WM;
+  const int mi = lane >> 3, mr = lane & 7;
+  uint32_t ah[KST][4], al[KST][4];
+  {
+    const int row = 16 * wm + (mi & 1) * 8 + mr;
+    const uint32_t base = smem_u32(sq) + row * C::QROW;
+#pragma unroll
+    for (int ks = 0; ks < KST; ++ks) {
+      const int ch = 2 * ks + (mi >> 1);
+      ldsm_x4(base + ((ch ^ (row & 7)) << 4), ah[ks][0], ah[ks][1], ah[ks][2],
+              ah[ks][3]);
+      ldsm_x4(base + (((ch + CH) ^ (row & 7)) << 4), al[ks][0], al[ks][1],
+              al[ks][2], al[ks][3]);
+    }
+  }
+  for (int ct = 0; ct < nct; ++ct) {
+    if (ct + 1 < nct) {
+      load_c(ct + 1);
+      cp_async_wait_but_one();
+    } else {
+      cp_async_wait_all();
+    }
+    __syncthreads();
+    const uint8_t* cb = sc + (ct & 1) * C::CBYTES;
+    const uint32_t ca = smem_u32(cb);
+    float acc[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) acc[nt][x] = 0.f;
+#pragma unroll
+    for (int p = 0; p < KST / 2; ++p) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = wn * (NT * 8) + nt * 8 + mr;
+        uint32_t r0, r1, r2, r3;
+        ldsm_x4(ca + row * (D * 2) + (((4 * p + mi) ^ (row & 7)) << 4), r0, r1,
+                r2, r3);
+        mma16816(acc[nt], ah[2 * p], r0, r1);
+        mma16816(acc[nt], al[2 * p], r0, r1);
+        mma16816(acc[nt], ah[2 * p + 1], r2, r3);
+        mma16816(acc[nt], al[2 * p + 1], r2, r3);
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int col = ct * kSelBlock + wn * (NT * 8) + nt * 8 + 2 * (lane & 3);
+      const int row = 16 * wm + (lane >> 2);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (isnan(acc[nt][x])) acc[nt][x] = -INFINITY;
+      *reinterpret_cast<float2*>(S + (size_t)row * a.ld + col) =
+          make_float2(acc[nt][0], acc[nt][1]);
+      *reinterpret_cast<float2*>(S + (size_t)(row + 8) * a.ld + col) =
+          make_float2(acc[nt][2], acc[nt][3]);
+    }
+    // the largest |c|^2 among the tile's blocks
+    float cm = 0.f;
+    for (int e = tid; e < kSelBlock * CH; e += 256) {
+      const int row = e / CH, ch = e % CH;
+      const uint4 w = *reinterpret_cast<const uint4*>(
+          cb + row * (D * 2) + ((ch ^ (row & 7)) << 4));
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+      float nn = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float lo = bf16lo(ww[i]), hi = bf16hi(ww[i]);
+        nn = fmaf(lo * kNormUp, lo * kNormUp, nn);
+        nn = fmaf(hi * kNormUp, hi * kNormUp, nn);
+      }
+#pragma unroll
+      for (int o = CH / 2; o; o >>= 1) nn += __shfl_xor_sync(~0u, nn, o);
+      cm = __uint_as_float(max(__float_as_uint(cm), __float_as_uint(fabsf(nn))));
+    }
+    const uint32_t cw = __reduce_max_sync(~0u, __float_as_uint(cm));
+    if (lane == 0) atomicMax(cmax_s, cw);
+    __syncthreads();
+  }
+  const float cmax = sqrtf(__uint_as_float(*cmax_s)) * kNormDown;
+  WarpGroup g;
+  for (int rr = warp; rr < nrow; rr += 8) {
+    const int row = row0 + rr;
+    const int last = (a.causal ? row + off : a.Lkv - 1) / kSelBlock;
+    const SelRange r = sel_range(last, a.n_sel, a.n_first, a.n_local);
+    const float eps = score_eps(nrm[rr], cmax);
+    int* out = a.sel + ((size_t)bh * a.Lq + row) * a.n_sel;
+    double qd[D / 32];
+    bool have_q = false;
+    select_row(g, S + (size_t)rr * a.ld + r.f, r.f, r.m1, r.end, r.k, a.n_sel,
+               eps, out, [&](int j) {
+                 if (!have_q) {
+                   have_q = true;
+                   const __nv_bfloat16* q =
+                       a.q + (((size_t)b * a.Hkv + h) * a.G * (size_t)a.Lq + row) * D;
+#pragma unroll
+                   for (int x = 0; x < D / 32; ++x) {
+                     qd[x] = 0.0;
+                     for (int gg = 0; gg < a.G; ++gg)
+                       qd[x] += (double)__bfloat162float(
+                           q[(size_t)gg * a.Lq * D + lane + 32 * x]);
+                   }
+                 }
+                 return exact_score<D>(qd, c0 + (size_t)j * D);
+               });
+    __syncwarp();
+  }
+}
+
+template <int D, int TM>
+cudaError_t launch_block_select_t(const SelectArgs& a0, int B,
+                                  cudaStream_t st) {
+  SelectArgs a = a0;
+  a.ntile = (a.Lq + TM - 1) / TM;
+  const int smem = SelectCfg<D, TM>::smem(a.ld);
+  const long long grid = (long long)a.ntile * B * a.Hkv;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(
+      block_select_kernel<D, TM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      smem);
+  if (e != cudaSuccess) return e;
+  block_select_kernel<D, TM><<<(unsigned)grid, 256, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+// Score columns a prompt tile keeps: whole 64-block tiles, plus 8 floats so
+// that the 8 rows a fragment store writes fall into different banks.
+inline int select_ld(int nblk) { return (nblk + 63) / 64 * 64 + 8; }
+
+template <int D>
+cudaError_t launch_block_select(SelectArgs a, int B, cudaStream_t st) {
+  a.ld = select_ld(a.nblk);
+  constexpr int kTwo = 113 * 1024;  // two CTAs per SM
+  if (SelectCfg<D, 64>::smem(a.ld) <= kTwo)
+    return launch_block_select_t<D, 64>(a, B, st);
+  if (SelectCfg<D, 32>::smem(a.ld) <= kTwo)
+    return launch_block_select_t<D, 32>(a, B, st);
+  return launch_block_select_t<D, 16>(a, B, st);
+}
+
+}  // namespace blasst

@@ -66,7 +66,13 @@ struct DecodeMmaArgs {
   int max_pages, num_pages, log2_page;
   int per_length;  // ln_lambda is ln a; sequence b uses min(0, ln a - ln L_b)
   const int* order;  // paged: sequence of each grid slot (NULL: slot b is b)
+  // block-selected decode (SEL): the blocks of each (sequence, KV head), any
+  // order; ids < 0 and repeated ids count for nothing
+  const int* sel;    // [B, Hkv, n_sel]
+  int n_sel;         // <= kSelDecodeMax
+  int kv_div;        // tiles of G heads per KV head
 };
+constexpr int kSelDecodeMax = 512;
 
 struct DecodeMmaCfg {
   static constexpr int BOX = 64 * 128;      // 64 rows x 128 bytes (64 dims)
@@ -157,12 +163,62 @@ __device__ __forceinline__ uint32_t swz_off_rows(int key, int chunk) {
   return (uint32_t)(line * 128 + (((chunk & 7) ^ (line & 7)) << 4));
 }
 
+// Distinct block ids of a selection, in order of first appearance, into
+// shared `list`; returns their number, or -1 after recording an id at or past
+// the sequence's blocks (nk).  Whole CTA of kDecThreads.
+__device__ __forceinline__ int sel_compact(const int* sel, int n_sel, int nk,
+                                           unsigned where, int* raw,
+                                           int* list) {
+  __shared__ int wsum[kDecThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  bool bad = false;
+  for (int e = tid; e < n_sel; e += kDecThreads) {
+    int id = __ldg(sel + e);
+    if (id >= nk) {
+      record_error(kBadBlockId, where, 0xffffffffu, (unsigned)id);
+      bad = true;
+    }
+    raw[e] = id;
+  }
+  if (__syncthreads_or(bad)) return -1;
+  int at = 0;
+  for (int e0 = 0; e0 < n_sel; e0 += kDecThreads) {
+    const int e = e0 + tid;
+    bool take = e < n_sel && raw[e] >= 0;
+    if (take) {
+      const int id = raw[e];
+      for (int x = 0; x < e; ++x)
+        if (raw[x] == id) {
+          take = false;
+          break;
+        }
+    }
+    const unsigned m = __ballot_sync(0xffffffffu, take);
+    if (lane == 0) wsum[warp] = __popc(m);
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kDecThreads / 32; ++w) {
+      if (w < warp) before += wsum[w];
+      total += wsum[w];
+    }
+    if (take) list[at + before + __popc(m & ((1u << lane) - 1u))] = raw[e];
+    at += total;
+    __syncthreads();
+  }
+  return at;
+}
+
 // BATCH = 2: the batched decision rule (contiguous cache): blocks r and
 // r+1 are scored before either is decided, and each is judged against
 // Mb = max(running max before r, maxima of both blocks); kept blocks use Mb
 // as the reference of P.  (A skip never moves the running max, so the
 // running max is always the reference of O and l, in both rules.)
-template <int G, int D, bool PAGED, int BATCH = 1>
+//
+// SEL: attention over a.sel's blocks only (paged, dense over those blocks):
+// the CTA lists its (sequence, KV head)'s distinct blocks in shared memory
+// and the splits divide that list instead of the sequence.
+template <int G, int D, bool PAGED, int BATCH = 1, bool SEL = false>
 __global__ void __launch_bounds__(kDecThreads, 3)
     decode_mma_kernel(const __grid_constant__ DecodeMmaArgs a) {
   static_assert(G >= 1 && G <= 8, "at most 8 heads per tile");
@@ -186,11 +242,16 @@ __global__ void __launch_bounds__(kDecThreads, 3)
   const int lane = tid & 31;
   const int warp = tid >> 5;
 
+  static_assert(!SEL || (PAGED && BATCH == 1), "selected blocks: paged");
+  __shared__ int sel_list[SEL ? kSelDecodeMax : 1];
+  __shared__ int sel_raw[SEL ? kSelDecodeMax : 1];
   const int s = blockIdx.x % a.S;
-  const int slot = blockIdx.x / a.S;  // sequence slot * Hkv + hkv
-  const int Hq = a.Hkv * G;
-  const int hkv = slot % a.Hkv;
-  int b = slot / a.Hkv;
+  const int slot = blockIdx.x / a.S;  // sequence slot * head tiles + tile
+  const int nht = SEL ? a.Hkv * a.kv_div : a.Hkv;  // tiles of G heads
+  const int Hq = nht * G;
+  const int ht = slot % nht;
+  const int hkv = SEL ? ht / a.kv_div : ht;
+  int b = slot / nht;
   if constexpr (PAGED) {
     if (a.order) b = __ldg(a.order + b);
   }
@@ -212,16 +273,40 @@ __global__ void __launch_bounds__(kDecThreads, 3)
   const int nk_b = (Lb + kDecBc - 1) / kDecBc;
   const int key_lo = (a.window > 0 && Lb > a.window) ? Lb - a.window : 0;
   const int jlo = key_lo / kDecBc;
-  const int j0 = jlo + (int)(((long long)s * (nk_b - jlo)) / a.S);
-  const int j1 = jlo + (int)(((long long)(s + 1) * (nk_b - jlo)) / a.S);
+  int n_all = nk_b - jlo;  // blocks the splits divide
+  if constexpr (SEL) {
+    n_all = sel_compact(a.sel + ((size_t)b * a.Hkv + hkv) * a.n_sel, a.n_sel,
+                        nk_b, (unsigned)(b * a.Hkv + hkv), sel_raw, sel_list);
+    if (n_all < 0) return;  // a bad id (uniform)
+  }
+  const int j0 = jlo + (int)(((long long)s * n_all) / a.S);
+  const int j1 = jlo + (int)(((long long)(s + 1) * n_all) / a.S);
   const int nblk = j1 - j0;
+  // block r of this split
+  auto blk = [&](int r) -> int {
+    if constexpr (SEL) return sel_list[j0 + r];
+    else return j0 + r;
+  };
   const int ps = 1 << a.log2_page;       // paged: rows per page
   const int seg = ps < 64 ? ps : 64;     // paged: rows per TMA segment
   if constexpr (PAGED) {
     // every page id this split reads, before any load
     bool bad = false;
+    if constexpr (SEL) {
+      const int per = kDecBc / seg;  // pages (or parts of one) per block
+      for (int x = tid; x < nblk * per; x += kDecThreads) {
+        const int t = blk(x / per) * kDecBc + (x % per) * seg;
+        if (t >= Lb) continue;
+        const int pg = t >> a.log2_page;
+        const int id = __ldg(bt_row + pg);
+        if (id < 0 || id >= a.num_pages) {
+          bad = true;
+          record_error(kBadPageId, (unsigned)b, (unsigned)pg, (unsigned)id);
+        }
+      }
+    }
     const int t0 = j0 * kDecBc, t1 = min(j1 * kDecBc, Lb);
-    if (t1 > t0)
+    if (!SEL && t1 > t0)
       for (int pg = (t0 >> a.log2_page) + tid; pg <= ((t1 - 1) >> a.log2_page);
            pg += kDecThreads) {
         const int id = __ldg(bt_row + pg);
@@ -281,7 +366,7 @@ __global__ void __launch_bounds__(kDecThreads, 3)
     prefetch_tmap(&a.tk);
     prefetch_tmap(&a.tv);
     for (int r = 0; r < nblk && r < C::NK; ++r)
-      load(&a.tk, sK + r * C::TILE, &kfull[r], j0 + r);
+      load(&a.tk, sK + r * C::TILE, &kfull[r], blk(r));
   }
 
   // A fragments of q (rows = heads; head h = lane / 4, zero for h >= G),
@@ -292,7 +377,7 @@ __global__ void __launch_bounds__(kDecThreads, 3)
   uint32_t qa[KST][2];
   {
     const uint32_t* qrow = reinterpret_cast<const uint32_t*>(
-        a.q + ((size_t)b * Hq + hkv * G + (hr < G ? hr : 0)) * D);
+        a.q + ((size_t)b * Hq + ht * G + (hr < G ? hr : 0)) * D);
 #pragma unroll
     for (int t = 0; t < KST; ++t) {
       qa[t][0] = hr < G ? __ldg(qrow + 8 * t + q4) : 0u;
@@ -366,7 +451,7 @@ __global__ void __launch_bounds__(kDecThreads, 3)
   // 16w + 8g + 2q4 + i, scaled, -inf where hidden); returns the block max of
   // head hr over the warp's keys.
   auto score = [&](int r, float (&sc)[2][2]) -> float {
-    const int j = j0 + r;
+    const int j = blk(r);
     const int stage = r % C::NK;
     if (!mbar_wait(&kfull[stage], (uint32_t)(r / C::NK) & 1u, kWaitDecodeK, r,
                    stage))
@@ -446,7 +531,7 @@ __global__ void __launch_bounds__(kDecThreads, 3)
 
   if constexpr (BATCH == 1) {
   for (int r = 0; r < nblk; ++r) {
-    const int j = j0 + r;
+    const int j = blk(r);
     const int stage = r % C::NK;
     float sc[2][2];
     const float mx = score(r, sc);
@@ -455,7 +540,7 @@ __global__ void __launch_bounds__(kDecThreads, 3)
     if (__syncthreads_or(!ok)) { ok = false; break; }
     // every warp has read K slot `stage`: refill it
     if (tid == 0 && r + C::NK < nblk)
-      load(&a.tk, sK + stage * C::TILE, &kfull[stage], j + C::NK);
+      load(&a.tk, sK + stage * C::TILE, &kfull[stage], blk(r + C::NK));
 
     // ---- decision (the same in every thread)
     float mt[G];
@@ -569,7 +654,7 @@ __global__ void __launch_bounds__(kDecThreads, 3)
       const float sum = red[(0 * 8 + g) * D + dd] + red[(1 * 8 + g) * D + dd] +
                         red[(2 * 8 + g) * D + dd] + red[(3 * 8 + g) * D + dd];
       const float l = sL[g] + sL[8 + g] + sL[16 + g] + sL[24 + g];
-      const size_t row = (size_t)b * Hq + hkv * G + g;
+      const size_t row = (size_t)b * Hq + ht * G + g;
       a.o_part[(row * a.S + s) * D + dd] = l > 0.f ? sum / l : 0.f;
       if (dd == 0)
         a.lse_part[row * a.S + s] = l > 0.f ? m_run[g] + __logf(l) : -INFINITY;

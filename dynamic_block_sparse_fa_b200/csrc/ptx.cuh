@@ -30,11 +30,14 @@ enum : unsigned int {
   kWaitMla = 15,
   kWaitDecodeWide = 16,
   kWaitMlaPair = 17,
+  kWaitSelect = 18,
   kWaitSelfTest = 99,
-  // Device-resident arguments found out of range (paged decode); these are
-  // reported as invalid arguments, not as waits that gave up.
+  // Device-resident arguments found out of range (paged calls, block
+  // selections); these are reported as invalid arguments, not as waits that
+  // gave up.
   kBadSeqLen = 100,
   kBadPageId = 101,
+  kBadBlockId = 102,
 };
 
 // About one second at B200 clocks: far beyond any legitimate wait of these

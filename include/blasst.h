@@ -497,6 +497,178 @@ size_t blasst_mla_decode_workspace_size(int B, int H, int num_splits);
 int blasst_mla_decode_splits(int B, int L);
 
 /*
+ * Block-selected attention: a cheap score picks the key blocks a query attends
+ * to, so that neither K nor V of the others is read.  (Not a form of BLASST,
+ * whose rule scores every block and drops the ones it finds negligible; the
+ * same long-context callers need both.)  Blocks are BLASST_SELECT_BLOCK = 64
+ * tokens; block j of a sequence holds its tokens [64 j, 64 j + 64).
+ *
+ *   c_j  = mean of the keys of block j                     blasst_block_means*
+ *   s_rj = sum over the heads g of a KV head of q_gr . c_j
+ *   row r takes its first n_first and its last n_local visible blocks, and
+ *   the best-scoring others until n_sel are taken          blasst_block_select*
+ *   o_r  = softmax over the selected, visible keys         blasst_select_*
+ *
+ * A selection is an int32 list per query row and KV head (its Hq/Hkv heads
+ * share it).  The attention entry points take any list: in any order, ids
+ * below 0 stand for no block, an id that appears twice counts once, and keys
+ * a causal row does not see are masked.  The list lives on the device and is
+ * checked there: an id past the last block (of the sequence, in decode) is
+ * not read through; blasst_check_device_error() then returns
+ * BLASST_ERR_INVALID_ARG (code 102).  The prefill calls ignore such an id, in
+ * decode the o and lse of that (sequence, KV head) are undefined.  A row that
+ * selected no visible key gives o = 0, lse = -inf and no gradient.
+ *
+ * Non-finite values: K and V rows of blocks that no query of a tile selected
+ * are not read.  The rows of a tile (128 Hkv/Hq neighbouring tokens of the
+ * heads of a KV head) share their blocks' V, so an infinity or NaN in a V row
+ * reaches every query of a tile that selected its block, masked or not.
+ */
+#define BLASST_SELECT_BLOCK 64
+
+/*
+ * blasst_block_means -- the mean of every block of keys, for the score.  The
+ * sum is float32 and is rounded once, to bf16 (a score needs no more, and the
+ * means are what every selection reads).
+ *
+ *  k       device bf16 [B,Hkv,Lkv,d]
+ *  means   device bf16 [B,Hkv,ceil(Lkv/64),d] (written); the last block's
+ *          mean is over the keys it has
+ *  d       64 or 128
+ */
+blasst_status_t blasst_block_means(const void *k, void *means, int B, int Hkv,
+                                   int Lkv, int d, void *stream);
+
+/*
+ * blasst_block_means_paged -- the means of a paged cache (pool, table and
+ * lengths as blasst_decode_paged), kept up to date while it grows.
+ *
+ *  n_new       tokens appended since the last call: the blocks that hold the
+ *              last n_new tokens of each sequence are computed (again); 0:
+ *              every block
+ *  means       device bf16 [B,Hkv,max_blocks,d]; other blocks, those past a
+ *              sequence's end among them, are left as they are
+ *  max_blocks  >= ceil(max_seq_len / 64)
+ * A bad length or page id is recorded as in blasst_decode_paged, and the mean
+ * it belongs to is not written.
+ */
+blasst_status_t blasst_block_means_paged(
+    const void *k_pages, long long page_stride, int num_pages, int page_size,
+    const int *block_table, int max_pages, const int *seq_lens,
+    int max_seq_len, int n_new, void *means, int max_blocks, int B, int Hkv,
+    int d, void *stream);
+
+/*
+ * blasst_block_select -- the selection of every row of a prompt.
+ *
+ *  q        device bf16 [B,Hq,Lq,d]
+ *  means    device bf16 [B,Hkv,ceil(Lkv/64),d]
+ *  sel      device int32 [B,Hkv,Lq,n_sel] (written): block ids ascending,
+ *           then -1
+ *  causal   row r sees keys up to r + Lkv - Lq (Lq <= Lkv); its last visible
+ *           block is the one that holds that key.  0: every block
+ *  n_sel    1 .. 4096 slots;  n_first, n_local >= 0, n_first + n_local <=
+ *           n_sel; causal calls need n_local >= 1 (the mean of the block a
+ *           row is in holds keys the row does not see)
+ *  d        64 or 128;  Hq/Hkv up to 32;  Lkv up to 131072
+ * The blocks taken are those of the exact scores (float32 first, float64
+ * where that leaves the cut in doubt), equal scores to the lower index.  A
+ * NaN score ranks lowest; one outside float32's range is an infinity.
+ */
+blasst_status_t blasst_block_select(const void *q, const void *means, int *sel,
+                                    int B, int Hq, int Hkv, int Lq, int Lkv,
+                                    int d, int causal, int n_sel, int n_first,
+                                    int n_local, void *stream);
+
+/*
+ * blasst_block_select_decode -- the same for one token per sequence, which
+ * sees all seq_lens[b] keys.
+ *
+ *  q           device bf16 [B,Hq,d]
+ *  means       device bf16 [B,Hkv,max_blocks,d]; rows past a sequence's
+ *              blocks are not read
+ *  seq_lens    device int32 [B], each in [0, max_seq_len] (checked on the
+ *              device); a length of 0 gives -1 in every slot
+ *  sel         device int32 [B,Hkv,n_sel] (written)
+ *  max_seq_len up to 1048576;  max_blocks >= ceil(max_seq_len / 64)
+ */
+blasst_status_t blasst_block_select_decode(const void *q, const void *means,
+                                           const int *seq_lens,
+                                           int max_seq_len, int max_blocks,
+                                           int *sel, int B, int Hq, int Hkv,
+                                           int d, int n_sel, int n_first,
+                                           int n_local, void *stream);
+
+/*
+ * blasst_select_prefill -- attention of every row of a prompt over the blocks
+ * its list selects.
+ *
+ *  q, k, v, o, lse  as blasst_prefill (lse may be NULL; o may not)
+ *  sel              device int32 [B,Hkv,Lq,n_sel]
+ *  d                64 or 128;  Hq/Hkv 1, 2, 4, 8, 16 or 32;  n_sel up to
+ *                   4096;  Lkv up to 262144;  scale > 0
+ *  workspace        device buffer of blasst_select_prefill_workspace_size()
+ *                   bytes, 256-byte aligned, caller-owned; contents need not
+ *                   be initialised
+ * Asynchronous on `stream`; two kernel launches; allocates nothing.
+ */
+size_t blasst_select_prefill_workspace_size(int B, int Hq, int Hkv, int Lq,
+                                            int Lkv);
+blasst_status_t blasst_select_prefill(const void *q, const void *k,
+                                      const void *v, const int *sel, void *o,
+                                      float *lse, int B, int Hq, int Hkv,
+                                      int Lq, int Lkv, int d, int n_sel,
+                                      float scale, int causal, void *workspace,
+                                      size_t workspace_bytes, void *stream);
+
+/*
+ * blasst_select_prefill_backward -- gradients of blasst_select_prefill with
+ * the selection held fixed (a list is a step function of q and k).
+ *
+ *  q, k, v, o, dout, lse, dq, dk, dv  as blasst_prefill_backward
+ *  sel        the forward's selection
+ *  d = 128; other limits as the forward
+ *  workspace  blasst_select_prefill_backward_workspace_size() bytes, 256-byte
+ *             aligned, caller-owned
+ * dQ is summed over key blocks in float32 by atomic additions, so its last
+ * bits depend on their order.  Asynchronous on `stream`; five or six kernel
+ * launches; allocates nothing.
+ */
+size_t blasst_select_prefill_backward_workspace_size(int B, int Hq, int Hkv,
+                                                     int Lq, int Lkv, int d);
+blasst_status_t blasst_select_prefill_backward(
+    const void *q, const void *k, const void *v, const void *o,
+    const void *dout, const float *lse, const int *sel, void *dq, void *dk,
+    void *dv, int B, int Hq, int Hkv, int Lq, int Lkv, int d, int n_sel,
+    float scale, int causal, void *workspace, size_t workspace_bytes,
+    void *stream);
+
+/*
+ * blasst_select_decode_paged -- one query token per sequence over the selected
+ * blocks of a paged cache, split over the list and merged as blasst_decode.
+ *
+ *  q, pools, table, lengths, o, lse  as blasst_decode_paged (o not NULL)
+ *  sel         device int32 [B,Hkv,n_sel], n_sel up to 512
+ *  d           64 or 128;  Hq/Hkv a power of two up to 256;  scale > 0
+ *  num_splits  1 .. n_sel, or 0 = blasst_select_decode_splits
+ *  workspace   blasst_decode_workspace_size(B, Hq, d, resolved num_splits)
+ * Only the pages of selected blocks are read; their table entries are checked
+ * on the device as in blasst_decode_paged.
+ */
+blasst_status_t blasst_select_decode_paged(
+    const void *q, const void *k_pages, const void *v_pages,
+    long long page_stride, int num_pages, int page_size,
+    const int *block_table, int max_pages, const int *seq_lens,
+    int max_seq_len, const int *sel, int n_sel, void *o, float *lse, int B,
+    int Hq, int Hkv, int d, float scale, int num_splits, void *workspace,
+    size_t workspace_bytes, void *stream);
+
+/* The automatic split count of blasst_select_decode_paged (pure function):
+ * the waves of (sequence, tile of up to 8 heads, split) items on 3 CTAs per
+ * SM times an item's blocks and its fixed cost, fewest splits on ties. */
+int blasst_select_decode_splits(int B, int Hq, int Hkv, int n_sel);
+
+/*
  * Calibration of the threshold lambda = a / L for a target sparsity
  * (gist.science summary, section 2 "Calibracao Automatica"; MLSys'26 reading
  * notes, observation 2: a is fitted on calibration data, not universal).
@@ -557,7 +729,7 @@ blasst_status_t blasst_skip_stats_reset(unsigned long long *counters,
  * device-resident argument was out of range: blasst_last_error() names the
  * sequence, the position and the value).  *where_out (may be NULL)
  * receives the code recorded first: 1..99 a wait, 100 a sequence length,
- * 101 a page id. */
+ * 101 a page id, 102 a block id of a selection. */
 blasst_status_t blasst_check_device_error(int *where_out);
 
 /* Diagnostic: launches one CTA that waits on an mbarrier nothing arrives
