@@ -701,59 +701,87 @@ def _nblk(L):
     return -(-L // SELECT_BLOCK)
 
 
-def _shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+def _addr(t, name, dtype, shape, dev, contiguous=True):
+    """Device address of a tensor argument after checking what the C ABI
+    cannot see: its type, shape (None: any) and device, dense in memory."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected "
                          f"{tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected "
+                         + (f"cuda:{dev}" if dev >= 0 else "a CUDA device"))
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
 
 
-def _device(*tensors):
-    """The one device all tensor arguments live on (None entries skipped)."""
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"tensors on several devices: {sorted(map(str, devs))}")
-    dev = devs.pop()
-    if dev.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device (got {dev})")
+def _device(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: must be a CUDA tensor (got {t.device})")
     return dev
 
 
 def _disjoint(outs, ins):
-    """Outputs (name, tensor) must not overlap an input or one another."""
+    """Outputs the caller passed (name, tensor) must not overlap an input or
+    one another."""
     for x, (name, t) in enumerate(outs):
         for other, u in ins + outs[x + 1:]:
             if _overlaps(t, u):
                 raise ValueError(f"{name} overlaps {other}")
 
 
+def _launch(name, dev, stream, *args):
+    """Calls the C entry point on the tensors' device and the given stream
+    (default: that device's current one)."""
+    raw = (torch._C._cuda_getCurrentRawStream(dev) if stream is None
+           else stream.cuda_stream)
+    if torch.cuda.current_device() == dev:
+        st = getattr(_lib, name)(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(_lib, name)(*args, raw)
+    if st != BLASST_OK:
+        raise BlasstError(st, name)
+
+
 def _pool(k_pages, v_pages=None):
     """(num_pages, Hkv, page_size, d, page stride) of a page pool's views."""
     P, Hkv, ps, d = k_pages.shape
-    for t in (k_pages, v_pages):
-        if t is None:
-            continue
-        if tuple(t.shape) != (P, Hkv, ps, d):
+    st = k_pages.stride()
+    if st[1:] != (ps * d, d, 1):
+        raise ValueError("pages must be contiguous inside a page")
+    if v_pages is not None:
+        if v_pages.shape != k_pages.shape:
             raise ValueError("k_pages / v_pages shapes")
-        if t.stride()[1:] != (ps * d, d, 1):
+        sv = v_pages.stride()
+        if sv[1:] != st[1:]:
             raise ValueError("pages must be contiguous inside a page")
-        if P > 1 and t.stride(0) != k_pages.stride(0):
+        if P > 1 and sv[0] != st[0]:
             raise ValueError("k_pages and v_pages must share the page stride")
     # (the stride of a pool of one page means nothing and may be any number)
-    return P, Hkv, ps, d, k_pages.stride(0) if P > 1 else Hkv * ps * d
+    return P, Hkv, ps, d, st[0] if P > 1 else Hkv * ps * d
+
+
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def blasst_block_means(k, *, means=None, stream=None):
     """Mean of every 64-key block: k [B,Hkv,L,d] bf16 -> [B,Hkv,nblk,d]."""
     B, Hkv, L, d = k.shape
-    dev = _device(k, means)
+    dev = _device(k, "k")
+    shape = (B, Hkv, _nblk(L), d)
     if means is None:
-        means = torch.empty(B, Hkv, _nblk(L), d, dtype=k.dtype, device=dev)
-    _shape(means, "means", (B, Hkv, _nblk(L), d))
-    _disjoint([("means", means)], [("k", k)])
-    with torch.cuda.device(dev):
-        _check(_lib.blasst_block_means(_arg(k, "k"), _arg(means, "means"), B,
-                                       Hkv, L, d, _stream(stream)),
-               "blasst_block_means")
+        means = k.new_empty(shape)
+    else:
+        _disjoint([("means", means)], [("k", k)])
+    _launch("blasst_block_means", dev, stream,
+            _addr(k, "k", _BF16, None, dev),
+            _addr(means, "means", _BF16, shape, dev), B, Hkv, L, d)
     return means
 
 
@@ -765,22 +793,19 @@ def blasst_block_means_paged(k_pages, block_table, seq_lens, means, *,
     as blasst_decode_paged; max_seq_len: host upper bound on the lengths
     (default: what the table and ``means`` hold)."""
     P, Hkv, ps, d, stride = _pool(k_pages)
-    dev = _device(k_pages, block_table, seq_lens, means)
+    dev = _device(k_pages, "k_pages")
     B, mp = block_table.shape
     nb = means.shape[2]
-    _shape(seq_lens, "seq_lens", (B,))
-    _shape(means, "means", (B, Hkv, nb, d))
-    _disjoint([("means", means)], [("block_table", block_table),
-                                   ("seq_lens", seq_lens)])
     if max_seq_len is None:
         max_seq_len = min(mp * ps, nb * SELECT_BLOCK)
-    with torch.cuda.device(dev):
-        _check(_lib.blasst_block_means_paged(
-            _arg(k_pages, "k_pages", contiguous=False), stride, P, ps,
-            _arg(block_table, "block_table", torch.int32), mp,
-            _arg(seq_lens, "seq_lens", torch.int32), int(max_seq_len),
-            int(n_new), _arg(means, "means"), nb, B, Hkv, d, _stream(stream)),
-            "blasst_block_means_paged")
+    _disjoint([("means", means)], [("block_table", block_table),
+                                   ("seq_lens", seq_lens)])
+    _launch("blasst_block_means_paged", dev, stream,
+            _addr(k_pages, "k_pages", _BF16, None, dev, False), stride, P, ps,
+            _addr(block_table, "block_table", _I32, None, dev), mp,
+            _addr(seq_lens, "seq_lens", _I32, (B,), dev), int(max_seq_len),
+            int(n_new), _addr(means, "means", _BF16, (B, Hkv, nb, d), dev), nb,
+            B, Hkv, d)
     return means
 
 
@@ -792,19 +817,17 @@ def blasst_block_select(q, means, Lkv, *, n_sel, n_first=1, n_local=1,
     visible blocks are always taken, the others by score."""
     B, Hq, Lq, d = q.shape
     Hkv = means.shape[1]
-    dev = _device(q, means, sel)
-    _shape(means, "means", (B, Hkv, _nblk(Lkv), d))
+    dev = _device(q, "q")
+    shape = (B, Hkv, Lq, max(int(n_sel), 0))
     if sel is None:
-        sel = torch.empty(B, Hkv, Lq, max(int(n_sel), 0), dtype=torch.int32,
-                          device=dev)
-    _shape(sel, "sel", (B, Hkv, Lq, n_sel))
-    _disjoint([("sel", sel)], [("q", q), ("means", means)])
-    with torch.cuda.device(dev):
-        _check(_lib.blasst_block_select(
-            _arg(q, "q"), _arg(means, "means"), _arg(sel, "sel", torch.int32),
-            B, Hq, Hkv, Lq, int(Lkv), d, int(bool(causal)), int(n_sel),
-            int(n_first), int(n_local), _stream(stream)),
-            "blasst_block_select")
+        sel = q.new_empty(shape, dtype=_I32)
+    else:
+        _disjoint([("sel", sel)], [("q", q), ("means", means)])
+    _launch("blasst_block_select", dev, stream,
+            _addr(q, "q", _BF16, None, dev),
+            _addr(means, "means", _BF16, (B, Hkv, _nblk(Lkv), d), dev),
+            _addr(sel, "sel", _I32, shape, dev), B, Hq, Hkv, Lq, int(Lkv), d,
+            int(bool(causal)), int(n_sel), int(n_first), int(n_local))
     return sel
 
 
@@ -815,24 +838,21 @@ def blasst_block_select_decode(q, means, seq_lens, *, n_sel, n_first=1,
     [B,Hkv,max_blocks,d], seq_lens [B] int32 -> int32 [B,Hkv,n_sel]."""
     B, Hq, d = q.shape
     Hkv, nb = means.shape[1], means.shape[2]
-    dev = _device(q, means, seq_lens, sel)
-    _shape(means, "means", (B, Hkv, nb, d))
-    _shape(seq_lens, "seq_lens", (B,))
+    dev = _device(q, "q")
+    shape = (B, Hkv, max(int(n_sel), 0))
     if sel is None:
-        sel = torch.empty(B, Hkv, max(int(n_sel), 0), dtype=torch.int32,
-                          device=dev)
-    _shape(sel, "sel", (B, Hkv, n_sel))
-    _disjoint([("sel", sel)], [("q", q), ("means", means),
-                               ("seq_lens", seq_lens)])
+        sel = q.new_empty(shape, dtype=_I32)
+    else:
+        _disjoint([("sel", sel)], [("q", q), ("means", means),
+                                   ("seq_lens", seq_lens)])
     if max_seq_len is None:
         max_seq_len = nb * SELECT_BLOCK
-    with torch.cuda.device(dev):
-        _check(_lib.blasst_block_select_decode(
-            _arg(q, "q"), _arg(means, "means"),
-            _arg(seq_lens, "seq_lens", torch.int32), int(max_seq_len), nb,
-            _arg(sel, "sel", torch.int32), B, Hq, Hkv, d, int(n_sel),
-            int(n_first), int(n_local), _stream(stream)),
-            "blasst_block_select_decode")
+    _launch("blasst_block_select_decode", dev, stream,
+            _addr(q, "q", _BF16, None, dev),
+            _addr(means, "means", _BF16, (B, Hkv, nb, d), dev),
+            _addr(seq_lens, "seq_lens", _I32, (B,), dev), int(max_seq_len), nb,
+            _addr(sel, "sel", _I32, shape, dev), B, Hq, Hkv, d, int(n_sel),
+            int(n_first), int(n_local))
     return sel
 
 
@@ -850,6 +870,13 @@ def blasst_select_decode_splits(B, Hq, Hkv, n_sel) -> int:
     return int(_lib.blasst_select_decode_splits(B, Hq, Hkv, n_sel))
 
 
+def _workspace(workspace, need, like):
+    """The caller's workspace, or a fresh one of `need` bytes."""
+    if workspace is not None:
+        return workspace
+    return like.new_empty(max(need, 1), dtype=torch.uint8)
+
+
 def blasst_select_prefill(q, k, v, sel, *, scale=None, causal=True, o=None,
                           lse=None, want_lse=True, workspace=None,
                           stream=None):
@@ -858,32 +885,30 @@ def blasst_select_prefill(q, k, v, sel, *, scale=None, causal=True, o=None,
     for none).  Returns (o, lse)."""
     B, Hq, Lq, d = q.shape
     Hkv, Lkv = k.shape[1], k.shape[2]
-    dev = _device(q, k, v, sel, o, lse, workspace)
-    _shape(k, "k", (B, Hkv, Lkv, d))
-    _shape(v, "v", k.shape)
+    dev = _device(q, "q")
     n_sel = sel.shape[-1]
-    _shape(sel, "sel", (B, Hkv, Lq, n_sel))
+    given = [(n, t) for n, t in (("o", o), ("lse", lse),
+                                 ("workspace", workspace)) if t is not None]
+    if given:
+        _disjoint(given, [("q", q), ("k", k), ("v", v), ("sel", sel)])
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    o = torch.empty_like(q) if o is None else o
-    _shape(o, "o", q.shape)
+    if o is None:
+        o = torch.empty_like(q)
     if lse is None and want_lse:
-        lse = torch.empty(B, Hq, Lq, dtype=torch.float32, device=dev)
-    if lse is not None:
-        _shape(lse, "lse", (B, Hq, Lq))
-    if workspace is None:
-        need = blasst_select_prefill_workspace_size(B, Hq, Hkv, Lq, Lkv)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _disjoint([("o", o), ("lse", lse), ("workspace", workspace)],
-              [("q", q), ("k", k), ("v", v), ("sel", sel)])
-    with torch.cuda.device(dev):
-        _check(_lib.blasst_select_prefill(
-            _arg(q, "q"), _arg(k, "k"), _arg(v, "v"),
-            _arg(sel, "sel", torch.int32), _arg(o, "o"),
-            _arg(lse, "lse", torch.float32), B, Hq, Hkv, Lq, Lkv, d, n_sel,
-            float(scale), int(bool(causal)), _arg(workspace, "workspace", None),
-            workspace.numel() * workspace.element_size(), _stream(stream)),
-            "blasst_select_prefill")
+        lse = q.new_empty((B, Hq, Lq), dtype=_F32)
+    ws = _workspace(workspace, _lib.blasst_select_prefill_workspace_size(
+        B, Hq, Hkv, Lq, Lkv), q)
+    _launch("blasst_select_prefill", dev, stream,
+            _addr(q, "q", _BF16, None, dev),
+            _addr(k, "k", _BF16, (B, Hkv, Lkv, d), dev),
+            _addr(v, "v", _BF16, (B, Hkv, Lkv, d), dev),
+            _addr(sel, "sel", _I32, (B, Hkv, Lq, n_sel), dev),
+            _addr(o, "o", _BF16, q.shape, dev),
+            None if lse is None else _addr(lse, "lse", _F32, (B, Hq, Lq), dev),
+            B, Hq, Hkv, Lq, Lkv, d, n_sel, float(scale), int(bool(causal)),
+            _addr(ws, "workspace", None, None, dev),
+            ws.numel() * ws.element_size())
     return o, lse
 
 
@@ -894,35 +919,33 @@ def blasst_select_prefill_backward(q, k, v, o, lse, dout, sel, *, scale=None,
     selection held fixed (d = 128); o and lse are that forward's."""
     B, Hq, Lq, d = q.shape
     Hkv, Lkv = k.shape[1], k.shape[2]
-    dev = _device(q, k, v, o, lse, dout, sel, dq, dk, dv, workspace)
+    dev = _device(q, "q")
     n_sel = sel.shape[-1]
+    given = [(n, t) for n, t in (("dq", dq), ("dk", dk), ("dv", dv),
+                                 ("workspace", workspace)) if t is not None]
+    if given:
+        _disjoint(given, [("q", q), ("k", k), ("v", v), ("o", o),
+                          ("lse", lse), ("dout", dout), ("sel", sel)])
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
-    for name, t, shape in (
-            ("k", k, (B, Hkv, Lkv, d)), ("v", v, k.shape), ("o", o, q.shape),
-            ("dout", dout, q.shape), ("lse", lse, (B, Hq, Lq)),
-            ("sel", sel, (B, Hkv, Lq, n_sel)), ("dq", dq, q.shape),
-            ("dk", dk, k.shape), ("dv", dv, k.shape)):
-        _shape(t, name, shape)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    if workspace is None:
-        need = blasst_select_prefill_backward_workspace_size(B, Hq, Hkv, Lq,
-                                                             Lkv, d)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _disjoint([("dq", dq), ("dk", dk), ("dv", dv), ("workspace", workspace)],
-              [("q", q), ("k", k), ("v", v), ("o", o), ("lse", lse),
-               ("dout", dout), ("sel", sel)])
-    with torch.cuda.device(dev):
-        _check(_lib.blasst_select_prefill_backward(
-            _arg(q, "q"), _arg(k, "k"), _arg(v, "v"), _arg(o, "o"),
-            _arg(dout, "dout"), _arg(lse, "lse", torch.float32),
-            _arg(sel, "sel", torch.int32), _arg(dq, "dq"), _arg(dk, "dk"),
-            _arg(dv, "dv"), B, Hq, Hkv, Lq, Lkv, d, n_sel, float(scale),
-            int(bool(causal)), _arg(workspace, "workspace", None),
-            workspace.numel() * workspace.element_size(), _stream(stream)),
-            "blasst_select_prefill_backward")
+    ws = _workspace(workspace,
+                    _lib.blasst_select_prefill_backward_workspace_size(
+                        B, Hq, Hkv, Lq, Lkv, d), q)
+    qs, ks = q.shape, (B, Hkv, Lkv, d)
+    _launch("blasst_select_prefill_backward", dev, stream,
+            _addr(q, "q", _BF16, None, dev), _addr(k, "k", _BF16, ks, dev),
+            _addr(v, "v", _BF16, ks, dev), _addr(o, "o", _BF16, qs, dev),
+            _addr(dout, "dout", _BF16, qs, dev),
+            _addr(lse, "lse", _F32, (B, Hq, Lq), dev),
+            _addr(sel, "sel", _I32, (B, Hkv, Lq, n_sel), dev),
+            _addr(dq, "dq", _BF16, qs, dev), _addr(dk, "dk", _BF16, ks, dev),
+            _addr(dv, "dv", _BF16, ks, dev), B, Hq, Hkv, Lq, Lkv, d, n_sel,
+            float(scale), int(bool(causal)),
+            _addr(ws, "workspace", None, None, dev),
+            ws.numel() * ws.element_size())
     return dq, dk, dv
 
 
@@ -936,42 +959,38 @@ def blasst_select_decode_paged(q, k_pages, v_pages, block_table, seq_lens, sel,
     ids are caught on the device: see blasst_check_device_error()."""
     B, Hq, d = q.shape
     P, Hkv, ps, d2, stride = _pool(k_pages, v_pages)
-    dev = _device(q, k_pages, v_pages, block_table, seq_lens, sel, o, lse,
-                  workspace)
     if d2 != d:
         raise ValueError(f"pages: head dimension {d2}, q has {d}")
+    dev = _device(q, "q")
     mp = block_table.shape[1]
     n_sel = sel.shape[-1]
-    _shape(block_table, "block_table", (B, mp))
-    _shape(seq_lens, "seq_lens", (B,))
-    _shape(sel, "sel", (B, Hkv, n_sel))
+    given = [(n, t) for n, t in (("o", o), ("lse", lse),
+                                 ("workspace", workspace)) if t is not None]
+    if given:
+        _disjoint(given, [("q", q), ("block_table", block_table),
+                          ("seq_lens", seq_lens), ("sel", sel)])
     if max_seq_len is None:
         max_seq_len = mp * ps
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    o = torch.empty_like(q) if o is None else o
-    _shape(o, "o", q.shape)
+    if o is None:
+        o = torch.empty_like(q)
     if lse is None and want_lse:
-        lse = torch.empty(B, Hq, dtype=torch.float32, device=dev)
-    if lse is not None:
-        _shape(lse, "lse", (B, Hq))
+        lse = q.new_empty((B, Hq), dtype=_F32)
     S = (num_splits if num_splits > 0
-         else blasst_select_decode_splits(B, Hq, Hkv, n_sel))
-    if workspace is None:
-        need = blasst_decode_workspace_size(B, Hq, d, S)
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
-    _disjoint([("o", o), ("lse", lse), ("workspace", workspace)],
-              [("q", q), ("block_table", block_table), ("seq_lens", seq_lens),
-               ("sel", sel)])
-    with torch.cuda.device(dev):
-        _check(_lib.blasst_select_decode_paged(
-            _arg(q, "q"), _arg(k_pages, "k_pages", contiguous=False),
-            _arg(v_pages, "v_pages", contiguous=False), stride, P, ps,
-            _arg(block_table, "block_table", torch.int32), mp,
-            _arg(seq_lens, "seq_lens", torch.int32), int(max_seq_len),
-            _arg(sel, "sel", torch.int32), n_sel, _arg(o, "o"),
-            _arg(lse, "lse", torch.float32), B, Hq, Hkv, d, float(scale), S,
-            _arg(workspace, "workspace", None),
-            workspace.numel() * workspace.element_size(), _stream(stream)),
-            "blasst_select_decode_paged")
+         else _lib.blasst_select_decode_splits(B, Hq, Hkv, n_sel))
+    ws = _workspace(workspace, _lib.blasst_decode_workspace_size(B, Hq, d, S),
+                    q)
+    _launch("blasst_select_decode_paged", dev, stream,
+            _addr(q, "q", _BF16, None, dev),
+            _addr(k_pages, "k_pages", _BF16, None, dev, False),
+            _addr(v_pages, "v_pages", _BF16, None, dev, False), stride, P, ps,
+            _addr(block_table, "block_table", _I32, (B, mp), dev), mp,
+            _addr(seq_lens, "seq_lens", _I32, (B,), dev), int(max_seq_len),
+            _addr(sel, "sel", _I32, (B, Hkv, n_sel), dev), n_sel,
+            _addr(o, "o", _BF16, q.shape, dev),
+            None if lse is None else _addr(lse, "lse", _F32, (B, Hq), dev),
+            B, Hq, Hkv, d, float(scale), S,
+            _addr(ws, "workspace", None, None, dev),
+            ws.numel() * ws.element_size())
     return o, lse

@@ -511,7 +511,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const float sl2 = p.scale * kPrefLog2e;
     int n = 0;
     bool ok = true;
-    uint32_t pk[64];  // P^T of a pair, from its P phase to its dS phase
+    // P^T of a pair, from its P phase to its dS phase: its bf16 values, or
+    // (SEL) fp16, whose 2^-11 keeps dS's own bf16 rounding the only one that
+    // counts (below 6e-5 fp16 is subnormal: off by 3e-8 of P = 1 at most)
+    uint32_t pk[64];
+    auto unpack_p = [](uint32_t w) -> float2 {
+      if constexpr (SEL)
+        return __half22float2(*reinterpret_cast<const __half2*>(&w));
+      else
+        return make_float2(bf16lo(w), bf16hi(w));
+    };
     // P^T of pair m (query tile i) into TMEM [0, 64); its lse in slot m & 1
     auto p_phase = [&](int m, int i) {
       const float* lse_m = lse_s + (m & 1) * 128;
@@ -561,6 +570,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (!ok) break;
           if (cc < 3) tmem_ld32(lane_base + (cc + 1) * 32, svb[(cc + 1) & 1]);
           const uint32_t (&sv)[32] = svb[cc & 1];
+          uint32_t st16[16];  // P^T of the chunk, bf16
           if (warp_full) {
 #pragma unroll
             for (int x = 0; x < 32; x += 4) {
@@ -569,8 +579,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               const float p1 = ex2_approx(fmaf(__uint_as_float(sv[x + 1]), sl2, -l4.y));
               const float p2 = ex2_approx(fmaf(__uint_as_float(sv[x + 2]), sl2, -l4.z));
               const float p3 = ex2_approx(fmaf(__uint_as_float(sv[x + 3]), sl2, -l4.w));
-              pk[cc * 16 + (x >> 1)] = pack_bf16x2(p0, p1);
-              pk[cc * 16 + (x >> 1) + 1] = pack_bf16x2(p2, p3);
+              st16[x >> 1] = pack_bf16x2(p0, p1);
+              st16[(x >> 1) + 1] = pack_bf16x2(p2, p3);
+              if constexpr (SEL) {
+                pk[cc * 16 + (x >> 1)] = pack_f16x2(p0, p1);
+                pk[cc * 16 + (x >> 1) + 1] = pack_f16x2(p2, p3);
+              }
             }
           } else {
 #pragma unroll
@@ -587,12 +601,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                               -lse_m[c]))
                             : 0.f;
             }
-            pk[cc * 16 + (x >> 1)] = pack_bf16x2(pv[0], pv[1]);
+            st16[x >> 1] = pack_bf16x2(pv[0], pv[1]);
+            if constexpr (SEL)
+              pk[cc * 16 + (x >> 1)] = pack_f16x2(pv[0], pv[1]);
           }
           }
-          uint32_t st16[16];
+          if constexpr (!SEL) {
 #pragma unroll
-          for (int u = 0; u < 16; ++u) st16[u] = pk[cc * 16 + u];
+            for (int u = 0; u < 16; ++u) pk[cc * 16 + u] = st16[u];
+          }
           tmem_st16(lane_base + 0 + cc * 16, st16);
           if (cc < 3) tc_wait_ld();
         }
@@ -638,14 +655,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int x = 0; x < 32; x += 4) {
             const float4 d4 =
                 reinterpret_cast<const float4*>(del_s)[(cc * 32 + x) >> 2];
-            const uint32_t pw0 = pk[cc * 16 + (x >> 1)];
-            const uint32_t pw1 = pk[cc * 16 + (x >> 1) + 1];
-            dk16[x >> 1] = pack_bf16x2(
-                bf16lo(pw0) * (__uint_as_float(dp[x]) - d4.x),
-                bf16hi(pw0) * (__uint_as_float(dp[x + 1]) - d4.y));
-            dk16[(x >> 1) + 1] = pack_bf16x2(
-                bf16lo(pw1) * (__uint_as_float(dp[x + 2]) - d4.z),
-                bf16hi(pw1) * (__uint_as_float(dp[x + 3]) - d4.w));
+            const float2 pa = unpack_p(pk[cc * 16 + (x >> 1)]);
+            const float2 pb = unpack_p(pk[cc * 16 + (x >> 1) + 1]);
+            dk16[x >> 1] =
+                pack_bf16x2(pa.x * (__uint_as_float(dp[x]) - d4.x),
+                            pa.y * (__uint_as_float(dp[x + 1]) - d4.y));
+            dk16[(x >> 1) + 1] =
+                pack_bf16x2(pb.x * (__uint_as_float(dp[x + 2]) - d4.z),
+                            pb.y * (__uint_as_float(dp[x + 3]) - d4.w));
           }
           tmem_st16(lane_base + 128 + cc * 16, dk16);
           // dS^T row rr, query columns 32cc..32cc+31: box cc/2, 16-byte

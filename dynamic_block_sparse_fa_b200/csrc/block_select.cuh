@@ -280,13 +280,76 @@ __device__ Cut find_cut(GroupT& g, const float* s, int n, int k) {
   return {a, a, b};
 }
 
+// The same cut for a warp whose n <= 32 NR finite scores fit its registers,
+// and the take itself: writes the k best of [f, f + n) ascending to out and
+// returns true when the cut is wider than 2 eps, else writes nothing.  A
+// prompt has a row per token and KV head, so this path sets the selection's
+// time; about 9 bisection steps of NR compares and one warp reduction.
+template <int NR>
+__device__ __forceinline__ bool take_clear(const float* s, int n, int k,
+                                           float eps, int f, int* out) {
+  const int lane = threadIdx.x & 31;
+  float v[NR];
+  float mx = -INFINITY, mn = INFINITY;
+#pragma unroll
+  for (int x = 0; x < NR; ++x) {
+    const int i = 32 * x + lane;
+    v[x] = i < n ? s[i] : -INFINITY;
+    mx = fmaxf(mx, v[x]);
+    mn = fminf(mn, i < n ? v[x] : INFINITY);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
+    mn = fminf(mn, __shfl_xor_sync(~0u, mn, o));
+  }
+  float lo = mn, hi = mx, t = mx;  // the first threshold tried is the maximum
+  for (;;) {
+    int c = 0;
+#pragma unroll
+    for (int x = 0; x < NR; ++x) c += v[x] >= t;
+    c = (int)__reduce_add_sync(~0u, (unsigned)c);
+    if (c == k) break;
+    if (c > k) {
+      if (t == mx) return false;  // more than k equal the largest
+      lo = t;
+    } else {
+      hi = t;
+    }
+    t = 0.5f * lo + 0.5f * hi;
+    if (!(t > lo && t < hi)) return false;  // equal values straddle the cut
+  }
+  float a = INFINITY, b = -INFINITY;
+#pragma unroll
+  for (int x = 0; x < NR; ++x) {
+    if (v[x] >= t) a = fminf(a, v[x]);
+    else b = fmaxf(b, v[x]);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a = fminf(a, __shfl_xor_sync(~0u, a, o));
+    b = fmaxf(b, __shfl_xor_sync(~0u, b, o));
+  }
+  if (!(a - b > 2.f * eps)) return false;
+#pragma unroll
+  for (int x = 0; x < NR; ++x) {
+    const unsigned m = __ballot_sync(~0u, v[x] >= t);
+    if (v[x] >= t) out[__popc(m & ((1u << lane) - 1u))] = f + 32 * x + lane;
+    out += __popc(m);
+  }
+  return true;
+}
+
 // Writes the row's n_sel slots: blocks [0, f), the best k of the candidates
 // [f, m1) whose approximate scores s[0 .. m1 - f) are off by at most eps
 // each, and [m1, end).  exact(j) (taken by a whole warp) is the float64
 // score of block j.  s is overwritten where the cut needs it.
-template <class GroupT, class ExactT>
-__device__ void select_row(GroupT& g, float* s, int f, int m1, int end, int k,
-                           int n_sel, float eps, int* out, ExactT exact) {
+// clear(at) may take the k candidates itself, to out + at (0 < k < m1 - f).
+template <class GroupT, class ClearT, class ExactT>
+__device__ __forceinline__ void select_row(GroupT& g, float* s, int f, int m1,
+                                           int end, int k, int n_sel, float eps,
+                                           int* out, ClearT clear,
+                                           ExactT exact) {
   const int n = m1 - f;
   const int lane = threadIdx.x & 31;
   int at = f;  // slots written so far
@@ -294,6 +357,8 @@ __device__ void select_row(GroupT& g, float* s, int f, int m1, int end, int k,
   if (k >= n) {
     for (int i = g.id; i < n; i += GroupT::kThreads) out[at + i] = f + i;
     at += n;
+  } else if (k > 0 && clear(at)) {
+    at += k;
   } else if (k > 0) {
     Cut c;
     bool again = !(eps < INFINITY);  // a bound that overflowed: all exact
@@ -312,20 +377,18 @@ __device__ void select_row(GroupT& g, float* s, int f, int m1, int end, int k,
       const float up = c.b + 2.f * eps, dn = c.a - 2.f * eps;
       const bool all = !(eps < INFINITY);
       g.sync();
-      for (int i = g.warp; i < n; i += g.nwarps) {
-        const float x = s[i];
-        float y;
-        if (!all && x > up) {
-          y = INFINITY;
-        } else if (!all && x < dn) {
-          y = -INFINITY;
-        } else {
-          const double e = exact(f + i) - (double)c.v;
-          // (a non-finite difference of a huge score: its own infinity)
-          y = isnan(e) ? -INFINITY : (float)e;
+      for (int i0 = 32 * g.warp; i0 < n; i0 += 32 * g.nwarps) {
+        const int i = i0 + lane;
+        const float x = i < n ? s[i] : 0.f;
+        float y = x > up ? INFINITY : -INFINITY;
+        unsigned todo = __ballot_sync(~0u, i < n && (all || !(x > up || x < dn)));
+        while (todo) {
+          const int t = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const double e = exact(f + i0 + t) - (double)c.v;
+          if (lane == t) y = isnan(e) ? -INFINITY : (float)e;
         }
-        __syncwarp();
-        if (lane == 0) s[i] = y;
+        if (i < n) s[i] = y;
       }
       g.sync();
       c = find_cut(g, s, n, k);
@@ -379,11 +442,13 @@ __device__ __forceinline__ SelRange sel_range(int last, int n_sel, int n_first,
   return r;
 }
 
-// Relative error bound of the float32 scores, against |sum_g |q_g|| |c|:
-// splitting the head sum into two bf16 parts loses 2^-18 of it, its float32
-// sum G 2^-24 <= 2^-19 (G <= 32), and the accumulation of d/8 + 16 partial
-// products at most 2^-23 each, 2^-18 for d = 128: together below 2^-16.
-constexpr float kSelEps = 1.52587890625e-05f;  // 2^-16
+// Relative error bounds of the float32 scores, against |sum_g |q_g|| |c|.
+// Tensor core: splitting the head sum into two bf16 parts loses 2^-16 of it,
+// its float32 sum G 2^-24 <= 2^-19 (G <= 32), and the accumulation of d/8
+// steps of 16 products about 2^-18: below 2^-15.  CUDA cores (no split): the
+// head sum 2^-19, 13 roundings of 2^-24 in the dot product: below 2^-18.
+constexpr float kSelEpsMma = 3.0517578125e-05f;   // 2^-15
+constexpr float kSelEpsFma = 3.814697265625e-06f;  // 2^-18
 // Norms are summed over values scaled by 2^40, so that squares of small
 // values stay above float32's smallest (a sum that overflows only sends the
 // row to the float64 scores).
@@ -392,8 +457,8 @@ constexpr float kNormUp = 1099511627776.f, kNormDown = 1.f / 1099511627776.f;
 // The error bound of a row whose |sum_g |q_g|| is nq, against means of norm
 // at most nc.  The product is formed first: where it overflows, so may the
 // scores, and the bound has to be infinite.
-__device__ __forceinline__ float score_eps(float nq, float nc) {
-  const float e = kSelEps * (nq * nc);
+__device__ __forceinline__ float score_eps(float rel, float nq, float nc) {
+  const float e = rel * (nq * nc);
   return nq > 0.f && nc > 0.f ? fmaxf(e, 1e-37f) : e;
 }
 
@@ -406,7 +471,7 @@ __device__ __forceinline__ double exact_score(const double (&qd)[D / 32],
   double e = 0.0;
 #pragma unroll
   for (int x = 0; x < D / 32; ++x)
-    e += qd[x] * (double)__bfloat162float(c[lane + 32 * x]);
+    e += qd[x] * (double)__bfloat162float(c[lane * (D / 32) + x]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) e += __shfl_xor_sync(~0u, e, o);
   return e;
@@ -517,12 +582,13 @@ __global__ void __launch_bounds__(kSelDecThreads)
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) qq += __shfl_xor_sync(~0u, qq, o);
-    eps = score_eps(sqrtf(qq) * kNormDown,
+    eps = score_eps(kSelEpsFma, sqrtf(qq) * kNormDown,
                     sqrtf(__uint_as_float(cmax_s)) * kNormDown);
   }
   double qd[D / 32];
   bool have_q = false;
   select_row(g, sel_smem, r.f, r.m1, r.end, r.k, a.n_sel, eps, out,
+             [](int) { return false; },
              [&](int j) {
                if (!have_q) {
                  have_q = true;
@@ -531,7 +597,7 @@ __global__ void __launch_bounds__(kSelDecThreads)
                    qd[x] = 0.0;
                    for (int gg = 0; gg < a.G; ++gg)
                      qd[x] += (double)__bfloat162float(
-                         q[(size_t)gg * D + lane + 32 * x]);
+                         q[(size_t)gg * D + lane * (D / 32) + x]);
                  }
                }
                return exact_score<D>(qd, c0 + (size_t)j * D);
@@ -765,12 +831,22 @@ __global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
     const int row = row0 + rr;
     const int last = (a.causal ? row + off : a.Lkv - 1) / kSelBlock;
     const SelRange r = sel_range(last, a.n_sel, a.n_first, a.n_local);
-    const float eps = score_eps(nrm[rr], cmax);
+    const float eps = score_eps(kSelEpsMma, nrm[rr], cmax);
     int* out = a.sel + ((size_t)bh * a.Lq + row) * a.n_sel;
     double qd[D / 32];
     bool have_q = false;
-    select_row(g, S + (size_t)rr * a.ld + r.f, r.f, r.m1, r.end, r.k, a.n_sel,
-               eps, out, [&](int j) {
+    float* srow = S + (size_t)rr * a.ld + r.f;
+    const int n = r.m1 - r.f;
+    select_row(g, srow, r.f, r.m1, r.end, r.k, a.n_sel, eps, out,
+               [&](int at) {
+                 if (!(eps < INFINITY)) return false;
+                 if (n <= 64) return take_clear<2>(srow, n, r.k, eps, r.f, out + at);
+                 if (n <= 128) return take_clear<4>(srow, n, r.k, eps, r.f, out + at);
+                 if (n <= 256) return take_clear<8>(srow, n, r.k, eps, r.f, out + at);
+                 if (n <= 512) return take_clear<16>(srow, n, r.k, eps, r.f, out + at);
+                 return false;
+               },
+               [&](int j) {
                  if (!have_q) {
                    have_q = true;
                    const __nv_bfloat16* q =
@@ -780,7 +856,7 @@ __global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
                      qd[x] = 0.0;
                      for (int gg = 0; gg < a.G; ++gg)
                        qd[x] += (double)__bfloat162float(
-                           q[(size_t)gg * a.Lq * D + lane + 32 * x]);
+                           q[(size_t)gg * a.Lq * D + lane * (D / 32) + x]);
                    }
                  }
                  return exact_score<D>(qd, c0 + (size_t)j * D);
