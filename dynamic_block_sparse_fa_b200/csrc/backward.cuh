@@ -69,14 +69,6 @@ struct BwdParams {
   const int* order;           // masked: grid slot of each CTA (null: own)
   int B, Hq, Hkv, Lq, Lkv, nq, nk, G, causal;
   float scale;
-  // SEL only.  A query tile is TQ tokens of the G heads of a KV head (nq
-  // such tiles); slot s keeps sel_count[s] of them, tile sel_list[s][i] with
-  // the token bits sel_words[s][i][2 halves of the key block][wpt].
-  const int* sel_count;
-  const int* sel_list;
-  const unsigned* sel_words;
-  int TQ, wpt;
-  unsigned rep;  // repeats a TQ-bit word over 32 bits (TQ < 32), else 1
 };
 
 constexpr int kBwdD = 128;
@@ -236,11 +228,6 @@ __global__ void __launch_bounds__(256) bwd_dq_kernel(const BwdParams p) {
   reinterpret_cast<uint4*>(p.dq)[i] = w;
 }
 
-// SEL: the pairs and their masks come from a block selection per token
-// (select_attn.cuh's tiles) instead of the forward's decision bytes.  The G
-// heads of a KV head are then rows of one tile, so a pair is (tile, key block)
-// and P is masked by the token bits of the two 64-key halves of the block.
-template <bool SEL>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     bwd_dkdv_kernel(const __grid_constant__ BwdParams p) {
   using C = BwdCfg;
@@ -269,32 +256,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     return __ldg(p.mask + ((size_t)(b * p.Hq + hq) * p.nq + i) * p.nk + jb) == 1;
   };
   // the next kept pair after (g, i) in (head, tile) order; false at the end
-  // (SEL: the next list position; the heads are rows of the tile)
-  const int n_list = SEL ? __ldg(p.sel_count + slot) : 0;
   auto next_kept = [&](int& g, int& i) -> bool {
     ++i;
-    if constexpr (SEL) {
-      return i < n_list;
-    } else {
-      while (g < p.G) {
-        if (i >= p.nq) {
-          ++g;
-          i = 0;
-          continue;
-        }
-        if (kept(g, i)) return true;
-        ++i;
+    while (g < p.G) {
+      if (i >= p.nq) {
+        ++g;
+        i = 0;
+        continue;
       }
-      return false;
+      if (kept(g, i)) return true;
+      ++i;
     }
-  };
-
-  // first query row (of each head) of tile i: SEL tiles are TQ tokens
-  auto row_of = [&](int i) -> int {
-    if constexpr (SEL)
-      return __ldg(p.sel_list + (size_t)slot * p.nq + i) * p.TQ;
-    else
-      return i * 128;
+    return false;
   };
 
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -347,11 +320,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       int n = 0;
       bool ok = true;
-      for (int g = 0; g < (SEL ? 1 : p.G) && ok; ++g) {
+      for (int g = 0; g < p.G && ok; ++g) {
         const int zq = b * p.Hq + hkv * p.G + g;
-        for (int i = 0; i < (SEL ? n_list : p.nq); ++i) {
-          if (!SEL && !kept(g, i)) continue;
-          const int r0 = row_of(i);
+        for (int i = 0; i < p.nq; ++i) {
+          if (!kept(g, i)) continue;
           const int s = n & 1;
           if (n >= 2 &&
               !mbar_wait(&bar[C::B_QE + s], ((n >> 1) - 1) & 1, kWaitBackward,
@@ -363,9 +335,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             tma_load_3d(smem + C::OFF_Q + s * C::TILE + c * C::BOX, &p.tq,
-                        &bar[C::B_QF + s], c * 64, r0, zq, pol_q);
+                        &bar[C::B_QF + s], c * 64, i * 128, zq, pol_q);
             tma_load_3d(smem + C::OFF_DO + s * C::TILE + c * C::BOX, &p.tdo,
-                        &bar[C::B_QF + s], c * 64, r0, zq, pol_q);
+                        &bar[C::B_QF + s], c * 64, i * 128, zq, pol_q);
           }
           // lse of pair n into slot s once pair n-2's P phase has read it
           if (n >= 2 &&
@@ -376,7 +348,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
           mbar_arrive_expect_tx(&bar[C::B_LF + s], 512);
           tma_load_3d(smem + C::OFF_LSE + s * 512, &p.tlse2, &bar[C::B_LF + s],
-                      r0, zq, 0, pol_q);
+                      i * 128, zq, 0, pol_q);
           // D of pair n once pair n-1's dS phase (its one reader) is over;
           // that phase needs this D's predecessor, so DSR cannot run ahead
           if (n >= 1 && !mbar_wait(&bar[C::B_DSR], (n - 1) & 1,
@@ -385,8 +357,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             break;
           }
           mbar_arrive_expect_tx(&bar[C::B_DF], 512);
-          tma_load_3d(smem + C::OFF_DEL, &p.tdel, &bar[C::B_DF], r0, zq, 0,
-                      pol_q);
+          tma_load_3d(smem + C::OFF_DEL, &p.tdel, &bar[C::B_DF], i * 128, zq,
+                      0, pol_q);
           ++n;
         }
       }
@@ -511,35 +483,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const float sl2 = p.scale * kPrefLog2e;
     int n = 0;
     bool ok = true;
-    // P^T of a pair, from its P phase to its dS phase: its bf16 values, or
-    // (SEL) fp16, whose 2^-11 keeps dS's own bf16 rounding the only one that
-    // counts (below 6e-5 fp16 is subnormal: off by 3e-8 of P = 1 at most)
-    uint32_t pk[64];
-    auto unpack_p = [](uint32_t w) -> float2 {
-      if constexpr (SEL)
-        return __half22float2(*reinterpret_cast<const __half2*>(&w));
-      else
-        return make_float2(bf16lo(w), bf16hi(w));
-    };
+    uint32_t pk[64];  // P^T of a pair, from its P phase to its dS phase
     // P^T of pair m (query tile i) into TMEM [0, 64); its lse in slot m & 1
     auto p_phase = [&](int m, int i) {
       const float* lse_m = lse_s + (m & 1) * 128;
-      // SEL: one bit per query column of each 32-column chunk, from the token
-      // bits of this key's half of the block and the causal limit
-      [[maybe_unused]] unsigned cm[4] = {0u, 0u, 0u, 0u};
-      if constexpr (SEL) {
-        const unsigned* w = p.sel_words +
-                            (((size_t)slot * p.nq + i) * 2 + (rr >> 6)) * p.wpt;
-        // first token of the tile that sees the key
-        const int t0 = p.causal ? key - off - row_of(i) : 0;
-#pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          const int wi = cc & (p.wpt - 1);
-          const int sh = t0 - wi * 32;
-          const unsigned see = sh <= 0 ? ~0u : sh >= 32 ? 0u : ~0u << sh;
-          cm[cc] = key_ok ? (__ldg(w + wi) & see) * p.rep : 0u;
-        }
-      }
       {
         const bool wl = ok && mbar_wait(&bar[C::B_LF + (m & 1)], (m >> 1) & 1,
                                         kWaitBackward, m, 33);
@@ -552,10 +499,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_after();
         // rows that see every query column of the tile need no mask; a warp
         // whose 32 rows all do takes the unmasked loop
-        const bool row_full =
-            SEL ? (cm[0] & cm[1] & cm[2] & cm[3]) == ~0u
-                : key_ok && i * 128 + 127 < p.Lq &&
-                      (!p.causal || key <= i * 128 + off);
+        const bool row_full = key_ok && i * 128 + 127 < p.Lq &&
+                              (!p.causal || key <= i * 128 + off);
         const bool warp_full = __all_sync(FULL, row_full);
         const float4* lse4 = reinterpret_cast<const float4*>(lse_m);
         // chunk cc + 1 is read while chunk cc is exponentiated; P of chunk
@@ -570,7 +515,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (!ok) break;
           if (cc < 3) tmem_ld32(lane_base + (cc + 1) * 32, svb[(cc + 1) & 1]);
           const uint32_t (&sv)[32] = svb[cc & 1];
-          uint32_t st16[16];  // P^T of the chunk, bf16
           if (warp_full) {
 #pragma unroll
             for (int x = 0; x < 32; x += 4) {
@@ -579,12 +523,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               const float p1 = ex2_approx(fmaf(__uint_as_float(sv[x + 1]), sl2, -l4.y));
               const float p2 = ex2_approx(fmaf(__uint_as_float(sv[x + 2]), sl2, -l4.z));
               const float p3 = ex2_approx(fmaf(__uint_as_float(sv[x + 3]), sl2, -l4.w));
-              st16[x >> 1] = pack_bf16x2(p0, p1);
-              st16[(x >> 1) + 1] = pack_bf16x2(p2, p3);
-              if constexpr (SEL) {
-                pk[cc * 16 + (x >> 1)] = pack_f16x2(p0, p1);
-                pk[cc * 16 + (x >> 1) + 1] = pack_f16x2(p2, p3);
-              }
+              pk[cc * 16 + (x >> 1)] = pack_bf16x2(p0, p1);
+              pk[cc * 16 + (x >> 1) + 1] = pack_bf16x2(p2, p3);
             }
           } else {
 #pragma unroll
@@ -594,22 +534,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int e = 0; e < 2; ++e) {
               const int c = cc * 32 + x + e;  // query column in the tile
               const int qr = i * 128 + c;
-              const bool valid = SEL ? (cm[cc] >> (x + e)) & 1u
-                                     : key_ok && qr < p.Lq &&
-                                           (!p.causal || key <= qr + off);
+              const bool valid = key_ok && qr < p.Lq &&
+                                 (!p.causal || key <= qr + off);
               pv[e] = valid ? ex2_approx(fmaf(__uint_as_float(sv[x + e]), sl2,
                                               -lse_m[c]))
                             : 0.f;
             }
-            st16[x >> 1] = pack_bf16x2(pv[0], pv[1]);
-            if constexpr (SEL)
-              pk[cc * 16 + (x >> 1)] = pack_f16x2(pv[0], pv[1]);
+            pk[cc * 16 + (x >> 1)] = pack_bf16x2(pv[0], pv[1]);
           }
           }
-          if constexpr (!SEL) {
+          uint32_t st16[16];
 #pragma unroll
-            for (int u = 0; u < 16; ++u) pk[cc * 16 + u] = st16[u];
-          }
+          for (int u = 0; u < 16; ++u) st16[u] = pk[cc * 16 + u];
           tmem_st16(lane_base + 0 + cc * 16, st16);
           if (cc < 3) tc_wait_ld();
         }
@@ -655,14 +591,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           for (int x = 0; x < 32; x += 4) {
             const float4 d4 =
                 reinterpret_cast<const float4*>(del_s)[(cc * 32 + x) >> 2];
-            const float2 pa = unpack_p(pk[cc * 16 + (x >> 1)]);
-            const float2 pb = unpack_p(pk[cc * 16 + (x >> 1) + 1]);
-            dk16[x >> 1] =
-                pack_bf16x2(pa.x * (__uint_as_float(dp[x]) - d4.x),
-                            pa.y * (__uint_as_float(dp[x + 1]) - d4.y));
-            dk16[(x >> 1) + 1] =
-                pack_bf16x2(pb.x * (__uint_as_float(dp[x + 2]) - d4.z),
-                            pb.y * (__uint_as_float(dp[x + 3]) - d4.w));
+            const uint32_t pw0 = pk[cc * 16 + (x >> 1)];
+            const uint32_t pw1 = pk[cc * 16 + (x >> 1) + 1];
+            dk16[x >> 1] = pack_bf16x2(
+                bf16lo(pw0) * (__uint_as_float(dp[x]) - d4.x),
+                bf16hi(pw0) * (__uint_as_float(dp[x + 1]) - d4.y));
+            dk16[(x >> 1) + 1] = pack_bf16x2(
+                bf16lo(pw1) * (__uint_as_float(dp[x + 2]) - d4.z),
+                bf16hi(pw1) * (__uint_as_float(dp[x + 3]) - d4.w));
           }
           tmem_st16(lane_base + 128 + cc * 16, dk16);
           // dS^T row rr, query columns 32cc..32cc+31: box cc/2, 16-byte
@@ -722,7 +658,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             named_sync(1, 128);
             if (warp == 2 && lane == 0) {
               tma_reduce_add_3d(&p.tdq, sDS + half * (C::TILE / 2), h * 32,
-                                row_of(i), b * p.Hq + hq);
+                                i * 128, b * p.Hq + hq);
               bulk_commit_group();
             }
           }
@@ -803,17 +739,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
 // 3-D map over the f32 dQ accumulator [planes, rows, 128], box 32 columns
 // (128 bytes) x 128 rows, 128-byte swizzle; rows past the end are clipped.
-// (box_rows x box_planes: 128 x 1, or the TQ tokens x G heads of a SEL tile)
 inline bool encode_map_f32(CUtensorMap* m, void* base, int rows,
-                           long long planes, int box_rows = 128,
-                           int box_planes = 1) {
+                           long long planes) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)kBwdD, (cuuint64_t)rows,
                         (cuuint64_t)planes};
   cuuint64_t strides[2] = {(cuuint64_t)kBwdD * 4,
                            (cuuint64_t)rows * kBwdD * 4};
-  cuuint32_t box[3] = {32, (cuuint32_t)box_rows, (cuuint32_t)box_planes};
+  cuuint32_t box[3] = {32, 128, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides,
                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -840,16 +774,14 @@ inline size_t bwd_workspace_bytes(int B, int Hq, int Lq) {
 }
 
 // [planes][cols] f32 with a 16-byte row stride, 128-column boxes of one row
-// (or TQ columns of G rows, SEL)
 inline bool encode_rows_f32(CUtensorMap* m, void* base, int cols,
-                            long long planes, int box_cols = 128,
-                            int box_rows = 1) {
+                            long long planes) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)planes, 1};
   cuuint64_t strides[2] = {(cuuint64_t)cols * 4,
                            (cuuint64_t)planes * cols * 4};
-  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+  cuuint32_t box[3] = {128, 1, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, base, dims, strides,
                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -918,12 +850,11 @@ inline cudaError_t launch_backward(const BwdProblem& pr, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     p.order = order;
   }
-  e = cudaFuncSetAttribute(bwd_dkdv_kernel<false>,
+  e = cudaFuncSetAttribute(bwd_dkdv_kernel,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            BwdCfg::SMEM_ALLOC);
   if (e != cudaSuccess) return e;
-  bwd_dkdv_kernel<false>
-      <<<(unsigned)grid, kBwdThreads, BwdCfg::SMEM_ALLOC, st>>>(p);
+  bwd_dkdv_kernel<<<(unsigned)grid, kBwdThreads, BwdCfg::SMEM_ALLOC, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   bwd_dq_kernel<<<(unsigned)conv_blocks, 256, 0, st>>>(p);

@@ -11,9 +11,9 @@
 // the same blocks, so the union is little longer than one list; at worst it
 // is all visible blocks, the dense forward's work.
 //
-// select_lists_kernel turns the selection into, per pair of tiles, the
-// ascending list of blocks any of its tokens selected and, per listed block,
-// one bit per token.  select_prefill_kernel is the two-tile pipeline of
+// select_lists_kernel turns the selection into, per pair of tiles (per tile
+// for the backward), the ascending list of blocks any of its tokens selected
+// and, per listed block, one bit per token.  select_prefill_kernel is the two-tile pipeline of
 // prefill2.cuh (a TMA producer warp, an MMA issuer warp, 4 softmax warps per
 // tile; S and O in tensor memory, P over S) walking that list two blocks (128
 // keys) a step; a tile none of whose tokens selected either block of a step
@@ -48,11 +48,12 @@ inline SelGeom sel_geom(int G, int Lq, int Lkv) {
 
 struct SelListArgs {
   const int* sel;   // [B, Hkv, Lq, n_sel]
-  int* nstep;       // [B*Hkv*npair]
-  unsigned* list;   // [B*Hkv*npair][cap]: block id | which tiles use it
-  unsigned* words;  // [B*Hkv*npair][cap][2 tiles][wpt]
+  int* nstep;       // [B*Hkv*nlist]
+  unsigned* list;   // [B*Hkv*nlist][cap]: block id | which tiles use it
+  unsigned* words;  // [B*Hkv*nlist][cap][tiles][wpt]
   int Lq, Lkv, n_sel, causal;
-  int TQ, wpt, npair, nblk, cap;
+  int TQ, wpt, nlist, nblk, cap;
+  int tiles;        // per list: 2 (forward pairs) or 1 (backward)
 };
 
 // Sets the bits of the selection rows [row0, row0 + nrow) in shared words
@@ -80,17 +81,17 @@ __device__ __forceinline__ void sel_set_bits(const int* sel, unsigned* bits,
 }
 
 __global__ void __launch_bounds__(256) select_lists_kernel(const SelListArgs a) {
-  extern __shared__ unsigned sel_bits[];  // [nblk][2 * wpt]
+  extern __shared__ unsigned sel_bits[];  // [nblk][tiles * wpt]
   __shared__ int wsum[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int bh = blockIdx.x / a.npair;
-  const int pair = blockIdx.x - bh * a.npair;
-  const int W = 2 * a.wpt;
+  const int bh = blockIdx.x / a.nlist;
+  const int id = blockIdx.x - bh * a.nlist;
+  const int W = a.tiles * a.wpt;
   for (int e = tid; e < a.nblk * W; e += 256) sel_bits[e] = 0u;
   __syncthreads();
-  const int row0 = pair * 2 * a.TQ;
+  const int row0 = id * a.tiles * a.TQ;
   sel_set_bits(a.sel + (size_t)bh * a.Lq * a.n_sel, sel_bits, W, a.TQ, row0,
-               min(2 * a.TQ, a.Lq - row0), a.n_sel, a.Lkv - a.Lq, a.causal,
+               min(a.tiles * a.TQ, a.Lq - row0), a.n_sel, a.Lkv - a.Lq, a.causal,
                a.nblk, (unsigned)bh);
   __syncthreads();
   unsigned* list = a.list + (size_t)blockIdx.x * a.cap;
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(256) select_lists_kernel(const SelListArgs a) 
     if (j < a.nblk)
       for (int w = 0; w < a.wpt; ++w) {
         any0 |= sel_bits[j * W + w];
-        any1 |= sel_bits[j * W + a.wpt + w];
+        if (a.tiles == 2) any1 |= sel_bits[j * W + a.wpt + w];
       }
     const bool take = (any0 | any1) != 0u;
     const unsigned m = __ballot_sync(~0u, take);
@@ -607,6 +608,36 @@ inline SelWorkspace sel_workspace(int B, int Hq, int Hkv, int Lq, int Lkv) {
   return w;
 }
 
+inline cudaError_t launch_select_lists(SelListArgs* a, const int* sel,
+                                       int* nstep, unsigned* list,
+                                       unsigned* words, const SelGeom& gm,
+                                       int BH, int Lq, int Lkv, int n_sel,
+                                       int causal, int tiles,
+                                       cudaStream_t st) {
+  a->sel = sel;
+  a->nstep = nstep;
+  a->list = list;
+  a->words = words;
+  a->Lq = Lq;
+  a->Lkv = Lkv;
+  a->n_sel = n_sel;
+  a->causal = causal;
+  a->TQ = gm.TQ;
+  a->wpt = gm.wpt;
+  a->nlist = tiles == 2 ? gm.npair : gm.ntile;
+  a->nblk = gm.nblk;
+  a->cap = gm.cap;
+  a->tiles = tiles;
+  const long long grid = (long long)BH * a->nlist;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  const int smem = gm.nblk * tiles * gm.wpt * 4;
+  cudaError_t e = cudaFuncSetAttribute(
+      select_lists_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  select_lists_kernel<<<(unsigned)grid, 256, smem, st>>>(*a);
+  return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t launch_select_prefill(const SelProblem& pr, cudaStream_t st) {
   using C = SelPrefillCfg<D>;
@@ -617,25 +648,11 @@ cudaError_t launch_select_prefill(const SelProblem& pr, cudaStream_t st) {
   const long long grid = (long long)pr.B * pr.Hkv * gm.npair;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   SelListArgs a;
-  a.sel = pr.sel;
-  a.nstep = reinterpret_cast<int*>(ws);
-  a.list = reinterpret_cast<unsigned*>(ws + w.list);
-  a.words = reinterpret_cast<unsigned*>(ws + w.words);
-  a.Lq = pr.Lq;
-  a.Lkv = pr.Lkv;
-  a.n_sel = pr.n_sel;
-  a.causal = pr.causal;
-  a.TQ = gm.TQ;
-  a.wpt = gm.wpt;
-  a.npair = gm.npair;
-  a.nblk = gm.nblk;
-  a.cap = gm.cap;
-  const int lsmem = gm.nblk * 2 * gm.wpt * 4;
-  cudaError_t e = cudaFuncSetAttribute(
-      select_lists_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lsmem);
-  if (e != cudaSuccess) return e;
-  select_lists_kernel<<<(unsigned)grid, 256, lsmem, st>>>(a);
-  e = cudaGetLastError();
+  cudaError_t e = launch_select_lists(
+      &a, pr.sel, reinterpret_cast<int*>(ws),
+      reinterpret_cast<unsigned*>(ws + w.list),
+      reinterpret_cast<unsigned*>(ws + w.words), gm, pr.B * pr.Hkv, pr.Lq,
+      pr.Lkv, pr.n_sel, pr.causal, 2, st);
   if (e != cudaSuccess) return e;
 
   SelPrefillParams p;
