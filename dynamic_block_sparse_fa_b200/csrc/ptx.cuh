@@ -311,6 +311,14 @@ __device__ __forceinline__ bool named_sync_and(uint32_t id, uint32_t nthreads,
   return out != 0;
 }
 
+// Read-only global load that stays where it is written: a prefetch the
+// compiler may not move down to its use.
+__device__ __forceinline__ uint32_t ld_nc_volatile(const unsigned* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 // ---------------------------------------------------------------------------
 // Math helpers
 // ---------------------------------------------------------------------------

@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(256)
   for (int e = threadIdx.x; e < a.nblk * a.wpt; e += 256) sel_bits[e] = 0u;
   __syncthreads();
   const int row0 = tile * a.TQ;
-  sel_set_bits(a.sel + (size_t)bh * a.Lq * a.n_sel, sel_bits, a.wpt, a.TQ, row0,
+  sel_set_bits(a.sel + (size_t)bh * a.Lq * a.n_sel, sel_bits, a.wpt, row0,
                min(a.TQ, a.Lq - row0), a.n_sel, a.Lkv - a.Lq, a.causal, a.nblk,
                (unsigned)bh);
   __syncthreads();
@@ -644,9 +644,9 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           tma_load_3d(dst + c * C::BOX, map, full, c * 64,
-                      (int)(e.x & kSelIdMask) * kSelBlock, bk, pol_kv);
+                      (int)e.x * kSelBlock, bk, pol_kv);
           tma_load_3d(dst + c * C::BOX + C::BOX / 2, map, full, c * 64,
-                      (int)(e.y & kSelIdMask) * kSelBlock, bk, pol_kv);
+                      (int)e.y * kSelBlock, bk, pol_kv);
         }
       };
       uint2 next = __ldg(list);
@@ -761,9 +761,8 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
     for (int s = 0; s < ns; ++s) {
       const unsigned bit = (w_n >> (tt & 31)) & 1u;
       // visible keys of the block for this row
-      const int nv = bit ? lim - (int)((h ? e_n.y : e_n.x) & kSelIdMask) *
-                                     kSelBlock + 1
-                         : 0;
+      const int nv =
+          bit ? lim - (int)(h ? e_n.y : e_n.x) * kSelBlock + 1 : 0;
       if (s + 1 < ns) {
         e_n = __ldg(list + s + 1);
         w_n = __ldg(wrow + (size_t)(2 * s + 2) * p.wpt);
@@ -1018,7 +1017,7 @@ inline cudaError_t launch_select_backward(const SelBwdProblem& pr,
   e = launch_select_lists(&la, pr.sel, reinterpret_cast<int*>(ws + w.nstep),
                           reinterpret_cast<unsigned*>(ws + w.list),
                           reinterpret_cast<unsigned*>(ws + w.words), gm, BH,
-                          pr.Lq, pr.Lkv, pr.n_sel, pr.causal, 1, st);
+                          pr.Lq, pr.Lkv, pr.n_sel, pr.causal, st);
   if (e != cudaSuccess) return e;
   p.nstep = la.nstep;
   p.list = la.list;
