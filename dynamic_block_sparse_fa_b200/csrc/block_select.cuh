@@ -136,6 +136,18 @@ __global__ void __launch_bounds__(128) block_means_kernel(const MeansArgs a) {
 // ---------------------------------------------------------------------------
 // Selection among the scores of one row
 // ---------------------------------------------------------------------------
+// Warp-wide maximum and minimum (one instruction each on sm_100).
+__device__ __forceinline__ float redux_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float redux_min(float x) {
+  float y;
+  asm volatile("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The threads that work on one row: a warp, or a whole CTA.
 struct WarpGroup {
   static constexpr int kThreads = 32;
@@ -143,11 +155,7 @@ struct WarpGroup {
   __device__ WarpGroup() : id(threadIdx.x & 31), warp(0), nwarps(1) {}
   __device__ void sync() { __syncwarp(); }
   __device__ int add(int x) { return (int)__reduce_add_sync(~0u, (unsigned)x); }
-  __device__ float max(float x) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
-    return x;
-  }
+  __device__ float max(float x) { return redux_max(x); }
   // exclusive rank of the set flags, and their number
   __device__ int rank(bool f, int& total) {
     const unsigned m = __ballot_sync(~0u, f);
@@ -183,9 +191,7 @@ struct CtaGroup {
     return t;
   }
   __device__ float max(float x) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
-    const uint32_t* s = share(__float_as_uint(x));
+    const uint32_t* s = share(__float_as_uint(redux_max(x)));
     float t = __uint_as_float(s[0]);
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) t = fmaxf(t, __uint_as_float(s[w]));
@@ -281,13 +287,17 @@ __device__ Cut find_cut(GroupT& g, const float* s, int n, int k) {
 }
 
 // The same cut for a warp whose n <= 32 NR finite scores fit its registers,
-// and the take itself: writes the k best of [f, f + n) ascending to out and
-// returns true when the cut is wider than 2 eps, else writes nothing.  A
+// and the take itself: writes the k best of [f, f + n) ascending to out.  A
 // prompt has a row per token and KV head, so this path sets the selection's
-// time; about 9 bisection steps of NR compares and one warp reduction.
-template <int NR>
-__device__ __forceinline__ bool take_clear(const float* s, int n, int k,
-                                           float eps, int f, int* out) {
+// time: about 9 bisection steps of NR compares and one warp reduction.  When
+// the cut is not wider than 2 eps, the blocks within 2 eps of it (2 or 3, on
+// a few rows of a hundred) get a lane each for their float64 score and are
+// ranked there.  Returns false, with nothing written, when they are more than
+// 32, or when equal scores straddle the cut and eps is 0.
+template <int NR, class ExactT>
+__device__ __forceinline__ bool take_rows(const float* s, int n, int k,
+                                          float eps, int f, int* out,
+                                          ExactT exact) {
   const int lane = threadIdx.x & 31;
   float v[NR];
   float mx = -INFINITY, mn = INFINITY;
@@ -298,43 +308,87 @@ __device__ __forceinline__ bool take_clear(const float* s, int n, int k,
     mx = fmaxf(mx, v[x]);
     mn = fminf(mn, i < n ? v[x] : INFINITY);
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-    mn = fminf(mn, __shfl_xor_sync(~0u, mn, o));
-  }
+  mx = redux_max(mx);
+  mn = redux_min(mn);
+  // at least k values are >= lo; fewer than k are >= hi, or hi is untried
   float lo = mn, hi = mx, t = mx;  // the first threshold tried is the maximum
+  bool split = false;              // t takes exactly k
   for (;;) {
     int c = 0;
 #pragma unroll
     for (int x = 0; x < NR; ++x) c += v[x] >= t;
     c = (int)__reduce_add_sync(~0u, (unsigned)c);
-    if (c == k) break;
+    if (c == k) {
+      split = true;
+      break;
+    }
     if (c > k) {
-      if (t == mx) return false;  // more than k equal the largest
       lo = t;
+      if (t == mx) break;  // more than k equal the largest
     } else {
       hi = t;
     }
     t = 0.5f * lo + 0.5f * hi;
-    if (!(t > lo && t < hi)) return false;  // equal values straddle the cut
+    if (!(t > lo && t < hi)) break;  // equal values straddle the cut
   }
-  float a = INFINITY, b = -INFINITY;
+  float a = lo, b = lo;
+  if (split) {
+    a = INFINITY;
+    b = -INFINITY;
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      if (v[x] >= t) a = fminf(a, v[x]);
+      else b = fmaxf(b, v[x]);
+    }
+    a = redux_min(a);
+    b = redux_max(b);
+  }
+  unsigned won = 0u;       // of the doubtful blocks, in ascending order
+  float up = t, dn = t;    // taken above up (or at it), left below dn
+  if (!split || !(a - b > 2.f * eps)) {
+    if (!split && eps == 0.f) return false;
+    up = b + 2.f * eps;
+    dn = a - 2.f * eps;
+    int sure = 0, cnt = 0;
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      sure += __popc(__ballot_sync(~0u, v[x] > up));
+      cnt += __popc(__ballot_sync(~0u, v[x] >= dn && v[x] <= up));
+    }
+    if (cnt > 32) return false;
+    double mine = 0.0;
+    int at = 0;
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      unsigned m = __ballot_sync(~0u, v[x] >= dn && v[x] <= up);
+      while (m) {
+        const int l = __ffs(m) - 1;
+        m &= m - 1;
+        const double e = exact(f + 32 * x + l);
+        if (lane == at) mine = e;
+        ++at;
+      }
+    }
+    int ahead = 0;  // doubtful blocks that go before this lane's
+    for (int o = 0; o < cnt; ++o) {
+      const double e = __shfl_sync(~0u, mine, o);
+      ahead += e > mine || (e == mine && o < lane);
+    }
+    won = __ballot_sync(~0u, lane < cnt && ahead < k - sure);
+  }
+  const bool clear = up == dn && won == 0u;
 #pragma unroll
   for (int x = 0; x < NR; ++x) {
-    if (v[x] >= t) a = fminf(a, v[x]);
-    else b = fmaxf(b, v[x]);
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    a = fminf(a, __shfl_xor_sync(~0u, a, o));
-    b = fmaxf(b, __shfl_xor_sync(~0u, b, o));
-  }
-  if (!(a - b > 2.f * eps)) return false;
-#pragma unroll
-  for (int x = 0; x < NR; ++x) {
-    const unsigned m = __ballot_sync(~0u, v[x] >= t);
-    if (v[x] >= t) out[__popc(m & ((1u << lane) - 1u))] = f + 32 * x + lane;
+    bool take = clear ? v[x] >= t : v[x] > up;
+    if (!clear) {
+      const bool doubt = v[x] >= dn && v[x] <= up;
+      const unsigned m = __ballot_sync(~0u, doubt);
+      take = take || (doubt && ((won >> __popc(m & ((1u << lane) - 1u))) & 1u));
+      const int c = __popc(m);
+      won = c < 32 ? won >> c : 0u;
+    }
+    const unsigned m = __ballot_sync(~0u, take);
+    if (take) out[__popc(m & ((1u << lane) - 1u))] = f + 32 * x + lane;
     out += __popc(m);
   }
   return true;
@@ -344,11 +398,11 @@ __device__ __forceinline__ bool take_clear(const float* s, int n, int k,
 // [f, m1) whose approximate scores s[0 .. m1 - f) are off by at most eps
 // each, and [m1, end).  exact(j) (taken by a whole warp) is the float64
 // score of block j.  s is overwritten where the cut needs it.
-// clear(at) may take the k candidates itself, to out + at (0 < k < m1 - f).
-template <class GroupT, class ClearT, class ExactT>
+// take_k(at) may take the k candidates itself, to out + at (0 < k < m1 - f).
+template <class GroupT, class TakeT, class ExactT>
 __device__ __forceinline__ void select_row(GroupT& g, float* s, int f, int m1,
                                            int end, int k, int n_sel, float eps,
-                                           int* out, ClearT clear,
+                                           int* out, TakeT take_k,
                                            ExactT exact) {
   const int n = m1 - f;
   const int lane = threadIdx.x & 31;
@@ -357,7 +411,7 @@ __device__ __forceinline__ void select_row(GroupT& g, float* s, int f, int m1,
   if (k >= n) {
     for (int i = g.id; i < n; i += GroupT::kThreads) out[at + i] = f + i;
     at += n;
-  } else if (k > 0 && clear(at)) {
+  } else if (k > 0 && take_k(at)) {
     at += k;
   } else if (k > 0) {
     Cut c;
@@ -837,30 +891,33 @@ __global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
     bool have_q = false;
     float* srow = S + (size_t)rr * a.ld + r.f;
     const int n = r.m1 - r.f;
-    select_row(g, srow, r.f, r.m1, r.end, r.k, a.n_sel, eps, out,
-               [&](int at) {
-                 if (!(eps < INFINITY)) return false;
-                 if (n <= 64) return take_clear<2>(srow, n, r.k, eps, r.f, out + at);
-                 if (n <= 128) return take_clear<4>(srow, n, r.k, eps, r.f, out + at);
-                 if (n <= 256) return take_clear<8>(srow, n, r.k, eps, r.f, out + at);
-                 if (n <= 512) return take_clear<16>(srow, n, r.k, eps, r.f, out + at);
-                 return false;
-               },
-               [&](int j) {
-                 if (!have_q) {
-                   have_q = true;
-                   const __nv_bfloat16* q =
-                       a.q + (((size_t)b * a.Hkv + h) * a.G * (size_t)a.Lq + row) * D;
+    auto exact = [&](int j) {
+      if (!have_q) {
+        have_q = true;
+        const __nv_bfloat16* q =
+            a.q + (((size_t)b * a.Hkv + h) * a.G * (size_t)a.Lq + row) * D;
 #pragma unroll
-                   for (int x = 0; x < D / 32; ++x) {
-                     qd[x] = 0.0;
-                     for (int gg = 0; gg < a.G; ++gg)
-                       qd[x] += (double)__bfloat162float(
-                           q[(size_t)gg * a.Lq * D + lane * (D / 32) + x]);
-                   }
-                 }
-                 return exact_score<D>(qd, c0 + (size_t)j * D);
-               });
+        for (int x = 0; x < D / 32; ++x) qd[x] = 0.0;
+        for (int gg = 0; gg < a.G; ++gg)
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x)
+            qd[x] += (double)__bfloat162float(
+                q[(size_t)gg * a.Lq * D + lane * (D / 32) + x]);
+      }
+      return exact_score<D>(qd, c0 + (size_t)j * D);
+    };
+    select_row(
+        g, srow, r.f, r.m1, r.end, r.k, a.n_sel, eps, out,
+        [&](int at) {
+          if (!(eps < INFINITY)) return false;
+          int* o = out + at;
+          if (n <= 64) return take_rows<2>(srow, n, r.k, eps, r.f, o, exact);
+          if (n <= 128) return take_rows<4>(srow, n, r.k, eps, r.f, o, exact);
+          if (n <= 256) return take_rows<8>(srow, n, r.k, eps, r.f, o, exact);
+          if (n <= 512) return take_rows<16>(srow, n, r.k, eps, r.f, o, exact);
+          return false;
+        },
+        exact);
     __syncwarp();
   }
 }
