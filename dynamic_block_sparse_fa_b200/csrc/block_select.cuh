@@ -286,52 +286,97 @@ __device__ Cut find_cut(GroupT& g, const float* s, int n, int k) {
   return {a, a, b};
 }
 
-// The same cut for a warp whose n <= 32 NR finite scores fit its registers,
-// and the take itself: writes the k best of [f, f + n) ascending to out.  A
-// prompt has a row per token and KV head, so this path sets the selection's
-// time: about 9 bisection steps of NR compares and one warp reduction.  When
-// the cut is not wider than 2 eps, the blocks within 2 eps of it (2 or 3, on
-// a few rows of a hundred) get a lane each for their float64 score and are
-// ranked there.  Returns false, with nothing written, when they are more than
-// 32, or when equal scores straddle the cut and eps is 0.
-template <int NR, class ExactT>
-__device__ __forceinline__ bool take_rows(const float* s, int n, int k,
-                                          float eps, int f, int* out,
-                                          ExactT exact) {
+// One row's candidates for a warp: the k best of blocks [f, f + n) by the
+// approximate scores s, each off by at most eps, go to out; 0 < k < n.
+struct RowTask {
+  const float* s;
+  int* out;
+  int f, n, k;
+  float eps;
+};
+
+// The same cut for R rows of one warp whose n <= 32 NR finite scores fit its
+// registers: t splits off exactly k (split), or equal values at t straddle
+// the cut.  A prompt has a row per token and KV head, so this sets the
+// selection's time: about 9 bisection steps of NR compares and one warp
+// reduction, two rows interleaved to cover each other's latency.
+template <int NR, int R>
+__device__ __forceinline__ void find_cuts(const RowTask (&r)[R],
+                                          float (&v)[R][NR], float (&t)[R],
+                                          bool (&split)[R]) {
   const int lane = threadIdx.x & 31;
-  float v[NR];
-  float mx = -INFINITY, mn = INFINITY;
+  float lo[R], hi[R], mx[R];
+  bool live[R];
 #pragma unroll
-  for (int x = 0; x < NR; ++x) {
-    const int i = 32 * x + lane;
-    v[x] = i < n ? s[i] : -INFINITY;
-    mx = fmaxf(mx, v[x]);
-    mn = fminf(mn, i < n ? v[x] : INFINITY);
-  }
-  mx = redux_max(mx);
-  mn = redux_min(mn);
-  // at least k values are >= lo; fewer than k are >= hi, or hi is untried
-  float lo = mn, hi = mx, t = mx;  // the first threshold tried is the maximum
-  bool split = false;              // t takes exactly k
-  for (;;) {
-    int c = 0;
+  for (int y = 0; y < R; ++y) {
+    mx[y] = -INFINITY;
+    lo[y] = INFINITY;
 #pragma unroll
-    for (int x = 0; x < NR; ++x) c += v[x] >= t;
-    c = (int)__reduce_add_sync(~0u, (unsigned)c);
-    if (c == k) {
-      split = true;
-      break;
+    for (int x = 0; x < NR; ++x) {
+      const int i = 32 * x + lane;
+      v[y][x] = i < r[y].n ? r[y].s[i] : -INFINITY;
+      mx[y] = fmaxf(mx[y], v[y][x]);
+      lo[y] = fminf(lo[y], i < r[y].n ? v[y][x] : INFINITY);
     }
-    if (c > k) {
-      lo = t;
-      if (t == mx) break;  // more than k equal the largest
-    } else {
-      hi = t;
-    }
-    t = 0.5f * lo + 0.5f * hi;
-    if (!(t > lo && t < hi)) break;  // equal values straddle the cut
   }
-  float a = lo, b = lo;
+  // at least k values are >= lo; fewer than k are >= hi, or hi is untried:
+  // the first threshold tried is the maximum
+#pragma unroll
+  for (int y = 0; y < R; ++y) {
+    mx[y] = redux_max(mx[y]);
+    lo[y] = redux_min(lo[y]);
+    hi[y] = mx[y];
+    t[y] = mx[y];
+    split[y] = false;
+    live[y] = true;
+  }
+  bool any = true;
+  while (any) {
+    int c[R];
+#pragma unroll
+    for (int y = 0; y < R; ++y) {
+      c[y] = 0;
+#pragma unroll
+      for (int x = 0; x < NR; ++x) c[y] += v[y][x] >= t[y];
+    }
+#pragma unroll
+    for (int y = 0; y < R; ++y)
+      c[y] = (int)__reduce_add_sync(~0u, (unsigned)c[y]);
+    any = false;
+#pragma unroll
+    for (int y = 0; y < R; ++y) {
+      if (!live[y]) continue;
+      if (c[y] == r[y].k) {
+        split[y] = true;
+        live[y] = false;
+        continue;
+      }
+      if (c[y] > r[y].k) lo[y] = t[y];
+      else hi[y] = t[y];
+      const float m = 0.5f * lo[y] + 0.5f * hi[y];
+      // equal values straddle the cut: at the maximum, or between neighbours
+      if (lo[y] == mx[y] || !(m > lo[y] && m < hi[y])) {
+        t[y] = lo[y];
+        live[y] = false;
+      } else {
+        t[y] = m;
+        any = true;
+      }
+    }
+  }
+}
+
+// The take of one row after its cut.  When the cut is not wider than 2 eps,
+// the blocks within 2 eps of it (2 or 3, on a few rows of a hundred) get a
+// lane each for their float64 score and are ranked there.  Returns false, with
+// nothing written, when they are more than 32, or when equal scores straddle
+// the cut and eps is 0.
+template <int NR, class ExactT>
+__device__ __forceinline__ bool take_cut(const RowTask& r, const float (&v)[NR],
+                                         float t, bool split, ExactT exact) {
+  const int lane = threadIdx.x & 31;
+  int* out = r.out;
+  float a = t, b = t;  // smallest taken, largest left
   if (split) {
     a = INFINITY;
     b = -INFINITY;
@@ -342,135 +387,134 @@ __device__ __forceinline__ bool take_rows(const float* s, int n, int k,
     }
     a = redux_min(a);
     b = redux_max(b);
-  }
-  unsigned won = 0u;       // of the doubtful blocks, in ascending order
-  float up = t, dn = t;    // taken above up (or at it), left below dn
-  if (!split || !(a - b > 2.f * eps)) {
-    if (!split && eps == 0.f) return false;
-    up = b + 2.f * eps;
-    dn = a - 2.f * eps;
-    int sure = 0, cnt = 0;
+    if (a - b > 2.f * r.eps) {
 #pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      sure += __popc(__ballot_sync(~0u, v[x] > up));
-      cnt += __popc(__ballot_sync(~0u, v[x] >= dn && v[x] <= up));
-    }
-    if (cnt > 32) return false;
-    double mine = 0.0;
-    int at = 0;
-#pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      unsigned m = __ballot_sync(~0u, v[x] >= dn && v[x] <= up);
-      while (m) {
-        const int l = __ffs(m) - 1;
-        m &= m - 1;
-        const double e = exact(f + 32 * x + l);
-        if (lane == at) mine = e;
-        ++at;
+      for (int x = 0; x < NR; ++x) {
+        const bool take = v[x] >= t;
+        const unsigned m = __ballot_sync(~0u, take);
+        if (take) out[__popc(m & ((1u << lane) - 1u))] = r.f + 32 * x + lane;
+        out += __popc(m);
       }
+      return true;
     }
-    int ahead = 0;  // doubtful blocks that go before this lane's
-    for (int o = 0; o < cnt; ++o) {
-      const double e = __shfl_sync(~0u, mine, o);
-      ahead += e > mine || (e == mine && o < lane);
-    }
-    won = __ballot_sync(~0u, lane < cnt && ahead < k - sure);
+  } else if (r.eps == 0.f) {
+    return false;
   }
-  const bool clear = up == dn && won == 0u;
+  const float up = b + 2.f * r.eps;  // above: taken for certain
+  const float dn = a - 2.f * r.eps;  // below: left for certain
+  int sure = 0, cnt = 0;
 #pragma unroll
   for (int x = 0; x < NR; ++x) {
-    bool take = clear ? v[x] >= t : v[x] > up;
-    if (!clear) {
-      const bool doubt = v[x] >= dn && v[x] <= up;
-      const unsigned m = __ballot_sync(~0u, doubt);
-      take = take || (doubt && ((won >> __popc(m & ((1u << lane) - 1u))) & 1u));
-      const int c = __popc(m);
-      won = c < 32 ? won >> c : 0u;
+    sure += __popc(__ballot_sync(~0u, v[x] > up));
+    cnt += __popc(__ballot_sync(~0u, v[x] >= dn && v[x] <= up));
+  }
+  if (cnt > 32) return false;
+  double mine = 0.0;
+  int at = 0;
+#pragma unroll 1
+  for (int x = 0; x < NR; ++x) {
+    float vx = v[0];
+#pragma unroll
+    for (int y = 1; y < NR; ++y) vx = x == y ? v[y] : vx;
+    unsigned m = __ballot_sync(~0u, vx >= dn && vx <= up);
+    while (m) {
+      const int l = __ffs(m) - 1;
+      m &= m - 1;
+      const double e = exact(r.f + 32 * x + l);
+      if (lane == at) mine = e;
+      ++at;
     }
-    const unsigned m = __ballot_sync(~0u, take);
-    if (take) out[__popc(m & ((1u << lane) - 1u))] = f + 32 * x + lane;
+  }
+  int ahead = 0;  // doubtful blocks that go before this lane's
+  for (int o = 0; o < cnt; ++o) {
+    const double e = __shfl_sync(~0u, mine, o);
+    ahead += e > mine || (e == mine && o < lane);
+  }
+  // of the doubtful blocks, in ascending order
+  unsigned won = __ballot_sync(~0u, lane < cnt && ahead < r.k - sure);
+#pragma unroll
+  for (int x = 0; x < NR; ++x) {
+    const bool doubt = v[x] >= dn && v[x] <= up;
+    unsigned m = __ballot_sync(~0u, doubt);
+    const bool take =
+        v[x] > up || (doubt && ((won >> __popc(m & ((1u << lane) - 1u))) & 1u));
+    const int c = __popc(m);
+    won = c < 32 ? won >> c : 0u;
+    m = __ballot_sync(~0u, take);
+    if (take) out[__popc(m & ((1u << lane) - 1u))] = r.f + 32 * x + lane;
     out += __popc(m);
   }
   return true;
 }
 
-// Writes the row's n_sel slots: blocks [0, f), the best k of the candidates
-// [f, m1) whose approximate scores s[0 .. m1 - f) are off by at most eps
-// each, and [m1, end).  exact(j) (taken by a whole warp) is the float64
-// score of block j.  s is overwritten where the cut needs it.
-// take_k(at) may take the k candidates itself, to out + at (0 < k < m1 - f).
-template <class GroupT, class TakeT, class ExactT>
-__device__ __forceinline__ void select_row(GroupT& g, float* s, int f, int m1,
-                                           int end, int k, int n_sel, float eps,
-                                           int* out, TakeT take_k,
-                                           ExactT exact) {
-  const int n = m1 - f;
+// The take of one row in general, by a warp or a CTA, for any n: s is
+// overwritten where the cut needs it.  exact(j) (taken by a whole warp) is the
+// float64 score of block j.
+template <class GroupT, class ExactT>
+__device__ void take_general(GroupT& g, float* s, const RowTask& r,
+                             ExactT exact) {
+  const int n = r.n, k = r.k;
+  const float eps = r.eps;
   const int lane = threadIdx.x & 31;
-  int at = f;  // slots written so far
-  for (int i = g.id; i < f; i += GroupT::kThreads) out[i] = i;
-  if (k >= n) {
-    for (int i = g.id; i < n; i += GroupT::kThreads) out[at + i] = f + i;
-    at += n;
-  } else if (k > 0 && take_k(at)) {
-    at += k;
-  } else if (k > 0) {
-    Cut c;
-    bool again = !(eps < INFINITY);  // a bound that overflowed: all exact
-    if (again) {
-      c = {0.f, -INFINITY, INFINITY};
-    } else {
-      c = find_cut(g, s, n, k);
-      // the scores are exact when eps is 0; otherwise the order is certain
-      // only when the cut is wider than the two errors
-      again = eps > 0.f && !(c.a - c.b > 2.f * eps);
-    }
-    if (again) {
-      // above b + 2 eps: better than every value left out; below a - 2 eps:
-      // worse than all k taken; between: the distance of the exact score to
-      // the cut, whose rounding to float32 is relative to that distance
-      const float up = c.b + 2.f * eps, dn = c.a - 2.f * eps;
-      const bool all = !(eps < INFINITY);
-      g.sync();
-      for (int i0 = 32 * g.warp; i0 < n; i0 += 32 * g.nwarps) {
-        const int i = i0 + lane;
-        const float x = i < n ? s[i] : 0.f;
-        float y = x > up ? INFINITY : -INFINITY;
-        unsigned todo = __ballot_sync(~0u, i < n && (all || !(x > up || x < dn)));
-        while (todo) {
-          const int t = __ffs(todo) - 1;
-          todo &= todo - 1;
-          const double e = exact(f + i0 + t) - (double)c.v;
-          if (lane == t) y = isnan(e) ? -INFINITY : (float)e;
-        }
-        if (i < n) s[i] = y;
-      }
-      g.sync();
-      c = find_cut(g, s, n, k);
-    }
-    // values above the cut, then equal ones in ascending index
-    int left = k;
-    {
-      int above = 0;
-      for (int i = g.id; i < n; i += GroupT::kThreads) above += s[i] > c.v;
-      left -= g.add(above);
-    }
-    for (int i0 = 0; i0 < n; i0 += GroupT::kThreads) {
-      const int i = i0 + g.id;
-      const float x = i < n ? s[i] : -INFINITY;
-      int total;
-      const bool eq = i < n && x == c.v;
-      const int er = g.rank(eq, total);
-      const bool take = i < n && (x > c.v || (eq && er < left));
-      left -= min(left, total);
-      const int r = g.rank(take, total);
-      if (take) out[at + r] = f + i;
-      at += total;
-    }
+  int* out = r.out;
+  Cut c;
+  bool again = !(eps < INFINITY);  // a bound that overflowed: all exact
+  if (again) {
+    c = {0.f, -INFINITY, INFINITY};
+  } else {
+    c = find_cut(g, s, n, k);
+    // the scores are exact when eps is 0; otherwise the order is certain
+    // only when the cut is wider than the two errors
+    again = eps > 0.f && !(c.a - c.b > 2.f * eps);
   }
-  for (int i = m1 + g.id; i < end; i += GroupT::kThreads) out[at + i - m1] = i;
-  at += end - m1;
-  for (int i = at + g.id; i < n_sel; i += GroupT::kThreads) out[i] = -1;
+  if (again) {
+    // above b + 2 eps: better than every value left out; below a - 2 eps:
+    // worse than all k taken; between: the distance of the exact score to
+    // the cut, whose rounding to float32 is relative to that distance
+    const float up = c.b + 2.f * eps, dn = c.a - 2.f * eps;
+    const bool all = !(eps < INFINITY);
+    g.sync();
+    for (int i0 = 32 * g.warp; i0 < n; i0 += 32 * g.nwarps) {
+      const int i = i0 + lane;
+      const float x = i < n ? s[i] : 0.f;
+      float y = x > up ? INFINITY : -INFINITY;
+      unsigned todo = __ballot_sync(~0u, i < n && (all || !(x > up || x < dn)));
+      while (todo) {
+        const int t = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const double e = exact(r.f + i0 + t) - (double)c.v;
+        if (lane == t) y = isnan(e) ? -INFINITY : (float)e;
+      }
+      if (i < n) s[i] = y;
+    }
+    g.sync();
+    c = find_cut(g, s, n, k);
+  }
+  // values above the cut, then equal ones in ascending index
+  int left = k;
+  {
+    int above = 0;
+    for (int i = g.id; i < n; i += GroupT::kThreads) above += s[i] > c.v;
+    left -= g.add(above);
+  }
+  for (int i0 = 0; i0 < n; i0 += GroupT::kThreads) {
+    const int i = i0 + g.id;
+    const float x = i < n ? s[i] : -INFINITY;
+    int total;
+    const bool eq = i < n && x == c.v;
+    const int er = g.rank(eq, total);
+    const bool take = i < n && (x > c.v || (eq && er < left));
+    left -= min(left, total);
+    const int rk = g.rank(take, total);
+    if (take) out[rk] = r.f + i;
+    out += total;
+  }
 }
+
+template <int N>
+struct IntTag {
+  static constexpr int value = N;
+};
 
 struct SelectArgs {
   const __nv_bfloat16* q;      // [B, Hq, Lq, d]; decode [B, Hq, d]
@@ -494,6 +538,24 @@ __device__ __forceinline__ SelRange sel_range(int last, int n_sel, int n_first,
   r.m1 = max(r.f, r.end - n_local);
   r.k = n_sel - r.f - (r.end - r.m1);
   return r;
+}
+
+// The slots that need no score: blocks [0, f) and [m1, end), all of [f, m1)
+// when they fit, and -1 behind them.  Returns whether k of [f, m1) are left to
+// be chosen (0 < k < m1 - f), for the slots from f on.
+template <class GroupT>
+__device__ __forceinline__ bool fill_fixed(GroupT& g, const SelRange& r,
+                                           int n_sel, int* out) {
+  const int n = r.m1 - r.f;
+  const int mid = min(r.k, n);  // slots of [f, m1)
+  const int used = r.f + mid + (r.end - r.m1);
+  const bool all = mid == n;
+  for (int i = g.id; i < n_sel; i += GroupT::kThreads) {
+    if (i >= used) out[i] = -1;
+    else if (i < r.f || all) out[i] = i;
+    else if (i >= r.f + mid) out[i] = r.m1 + i - r.f - mid;
+  }
+  return !all && mid > 0;
 }
 
 // Relative error bounds of the float32 scores, against |sum_g |q_g|| |c|.
@@ -641,21 +703,21 @@ __global__ void __launch_bounds__(kSelDecThreads)
   }
   double qd[D / 32];
   bool have_q = false;
-  select_row(g, sel_smem, r.f, r.m1, r.end, r.k, a.n_sel, eps, out,
-             [](int) { return false; },
-             [&](int j) {
-               if (!have_q) {
-                 have_q = true;
+  if (!fill_fixed(g, r, a.n_sel, out)) return;
+  const RowTask task = {sel_smem, out + r.f, r.f, n, r.k, eps};
+  take_general(g, sel_smem, task, [&](int j) {
+    if (!have_q) {
+      have_q = true;
 #pragma unroll
-                 for (int x = 0; x < D / 32; ++x) {
-                   qd[x] = 0.0;
-                   for (int gg = 0; gg < a.G; ++gg)
-                     qd[x] += (double)__bfloat162float(
-                         q[(size_t)gg * D + lane * (D / 32) + x]);
-                 }
-               }
-               return exact_score<D>(qd, c0 + (size_t)j * D);
-             });
+      for (int x = 0; x < D / 32; ++x) {
+        qd[x] = 0.0;
+        for (int gg = 0; gg < a.G; ++gg)
+          qd[x] += (double)__bfloat162float(
+              q[(size_t)gg * D + lane * (D / 32) + x]);
+      }
+    }
+    return exact_score<D>(qd, c0 + (size_t)j * D);
+  });
 }
 
 template <int D>
@@ -881,21 +943,31 @@ __global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
   }
   const float cmax = sqrtf(__uint_as_float(*cmax_s)) * kNormDown;
   WarpGroup g;
-  for (int rr = warp; rr < nrow; rr += 8) {
-    const int row = row0 + rr;
-    const int last = (a.causal ? row + off : a.Lkv - 1) / kSelBlock;
-    const SelRange r = sel_range(last, a.n_sel, a.n_first, a.n_local);
-    const float eps = score_eps(kSelEpsMma, nrm[rr], cmax);
-    int* out = a.sel + ((size_t)bh * a.Lq + row) * a.n_sel;
+  // two rows at a time
+  for (int rr = 2 * warp; rr < nrow; rr += 16) {
+    RowTask task[2];
+    bool todo[2];
+    int nmax = 0;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int row = row0 + min(rr + y, nrow - 1);
+      const int last = (a.causal ? row + off : a.Lkv - 1) / kSelBlock;
+      const SelRange r = sel_range(last, a.n_sel, a.n_first, a.n_local);
+      int* out = a.sel + ((size_t)bh * a.Lq + row) * a.n_sel;
+      todo[y] = rr + y < nrow && fill_fixed(g, r, a.n_sel, out);
+      task[y] = {S + (size_t)(row - row0) * a.ld + r.f, out + r.f, r.f,
+                 r.m1 - r.f, r.k, score_eps(kSelEpsMma, nrm[row - row0], cmax)};
+      if (todo[y]) nmax = max(nmax, task[y].n);
+    }
+    if (!todo[0] && !todo[1]) continue;
+    // the float64 score of block j for row y
     double qd[D / 32];
-    bool have_q = false;
-    float* srow = S + (size_t)rr * a.ld + r.f;
-    const int n = r.m1 - r.f;
-    auto exact = [&](int j) {
-      if (!have_q) {
-        have_q = true;
+    int have = -1;
+    auto exact = [&](int y, int j) {
+      if (have != y) {
+        have = y;
         const __nv_bfloat16* q =
-            a.q + (((size_t)b * a.Hkv + h) * a.G * (size_t)a.Lq + row) * D;
+            a.q + (((size_t)b * a.Hkv + h) * a.G * (size_t)a.Lq + row0 + rr + y) * D;
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) qd[x] = 0.0;
         for (int gg = 0; gg < a.G; ++gg)
@@ -906,18 +978,37 @@ __global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
       }
       return exact_score<D>(qd, c0 + (size_t)j * D);
     };
-    select_row(
-        g, srow, r.f, r.m1, r.end, r.k, a.n_sel, eps, out,
-        [&](int at) {
-          if (!(eps < INFINITY)) return false;
-          int* o = out + at;
-          if (n <= 64) return take_rows<2>(srow, n, r.k, eps, r.f, o, exact);
-          if (n <= 128) return take_rows<4>(srow, n, r.k, eps, r.f, o, exact);
-          if (n <= 256) return take_rows<8>(srow, n, r.k, eps, r.f, o, exact);
-          if (n <= 512) return take_rows<16>(srow, n, r.k, eps, r.f, o, exact);
-          return false;
-        },
-        exact);
+    // rows the register path cannot take stay to do
+    auto fast = [&](auto nr_tag) {
+      constexpr int NR = decltype(nr_tag)::value;
+      float v[2][NR], t[2];
+      bool split[2];
+      RowTask rt[2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        rt[y] = task[y];
+        if (!todo[y]) rt[y] = task[y ^ 1];  // (a finished row shadows the other)
+      }
+      find_cuts<NR, 2>(rt, v, t, split);
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        if (todo[y])
+          todo[y] = !take_cut<NR>(task[y], v[y], t[y], split[y],
+                                  [&](int j) { return exact(y, j); });
+    };
+    if ((!todo[0] || task[0].eps < INFINITY) &&
+        (!todo[1] || task[1].eps < INFINITY)) {
+      if (nmax <= 64) fast(IntTag<2>());
+      else if (nmax <= 128) fast(IntTag<4>());
+      else if (nmax <= 256) fast(IntTag<8>());
+      else if (nmax <= 512) fast(IntTag<16>());
+    }
+#pragma unroll 1
+    for (int y = 0; y < 2; ++y) {
+      if (!todo[y]) continue;
+      const RowTask rt = y ? task[1] : task[0];
+      take_general(g, S + (rt.s - S), rt, [&](int j) { return exact(y, j); });
+    }
     __syncwarp();
   }
 }
