@@ -740,7 +740,7 @@ def _launch(name, dev, stream, *args):
     (default: that device's current one)."""
     raw = (torch._C._cuda_getCurrentRawStream(dev) if stream is None
            else stream.cuda_stream)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = getattr(_lib, name)(*args, raw)
     else:
         with torch.cuda.device(dev):

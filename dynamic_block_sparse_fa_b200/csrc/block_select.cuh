@@ -601,7 +601,7 @@ __device__ __forceinline__ double exact_score(const double (&qd)[D / 32],
 constexpr int kSelDecThreads = 512;
 
 template <int D>
-__global__ void __launch_bounds__(kSelDecThreads)
+__global__ void __launch_bounds__(kSelDecThreads, 2)
     block_select_decode_kernel(const SelectArgs a) {
   constexpr int CH = D / 8;           // lanes per block row
   constexpr int RPW = 32 / CH;        // rows a warp reads at once
@@ -632,6 +632,7 @@ __global__ void __launch_bounds__(kSelDecThreads)
   if (tid == 0) cmax_s = 0u;
   if (tid < D) {
     float x = 0.f, y = 0.f;
+#pragma unroll 4
     for (int g = 0; g < a.G; ++g) {
       const float z = __bfloat162float(q[(size_t)g * D + tid]);
       x += z;
@@ -687,7 +688,6 @@ __global__ void __launch_bounds__(kSelDecThreads)
     if (lane == 0) atomicMax(&cmax_s, cw);
   }
   __syncthreads();
-  CtaGroup<kSelDecThreads> g(scratch);
   float eps = 0.f;
   if (r.k > 0 && r.k < n) {
     float qq = 0.f;
@@ -703,9 +703,8 @@ __global__ void __launch_bounds__(kSelDecThreads)
   }
   double qd[D / 32];
   bool have_q = false;
-  if (!fill_fixed(g, r, a.n_sel, out)) return;
   const RowTask task = {sel_smem, out + r.f, r.f, n, r.k, eps};
-  take_general(g, sel_smem, task, [&](int j) {
+  auto exact = [&](int j) {
     if (!have_q) {
       have_q = true;
 #pragma unroll
@@ -717,7 +716,33 @@ __global__ void __launch_bounds__(kSelDecThreads)
       }
     }
     return exact_score<D>(qd, c0 + (size_t)j * D);
-  });
+  };
+  // One warp's registers hold the scores of up to 1024 blocks (65536
+  // tokens): its reductions cost an instruction where the CTA's cost a
+  // barrier.  The other warps are done.
+  __shared__ int by_cta;
+  if (warp == 0) {
+    WarpGroup wg;
+    bool todo = fill_fixed(wg, r, a.n_sel, out);
+    if (todo && eps < INFINITY) {
+      auto fast = [&](auto nr_tag) {
+        constexpr int NR = decltype(nr_tag)::value;
+        const RowTask rt[1] = {task};
+        float v[1][NR], t[1];
+        bool split[1];
+        find_cuts<NR, 1>(rt, v, t, split);
+        todo = !take_cut<NR>(task, v[0], t[0], split[0], exact);
+      };
+      if (n <= 256) fast(IntTag<8>());
+      else if (n <= 512) fast(IntTag<16>());
+      else if (n <= 1024) fast(IntTag<32>());
+    }
+    if (lane == 0) by_cta = todo;
+  }
+  __syncthreads();
+  if (!by_cta) return;
+  CtaGroup<kSelDecThreads> g(scratch);
+  take_general(g, sel_smem, task, exact);
 }
 
 template <int D>

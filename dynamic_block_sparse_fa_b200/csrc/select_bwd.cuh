@@ -104,25 +104,22 @@ __global__ void __launch_bounds__(128)
 }
 
 // order[rank of slot s] = s, rank = slots with more tiles, or as many and a
-// lower index: a permutation of 0 .. n-1, the longest lists first.
+// lower index: a permutation of 0 .. n-1, the longest lists first.  A warp per
+// slot.
 __global__ void __launch_bounds__(256)
     select_order_kernel(const int* count, int n, int* order) {
-  __shared__ int tile[2048];
-  const int s = blockIdx.x * 256 + threadIdx.x;
-  const int cs = s < n ? count[s] : 0;
+  const int s = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (s >= n) return;
+  const int cs = __ldg(count + s);
   int rank = 0;
-  for (int t0 = 0; t0 < n; t0 += 2048) {
-    const int m = min(2048, n - t0);
-    __syncthreads();
-    for (int u = threadIdx.x; u < m; u += 256) tile[u] = count[t0 + u];
-    __syncthreads();
-    if (s < n)
-      for (int u = 0; u < m; ++u) {
-        const int cu = tile[u];
-        rank += (cu > cs) || (cu == cs && t0 + u < s);
-      }
+#pragma unroll 4
+  for (int u = lane; u < n; u += 32) {
+    const int cu = __ldg(count + u);
+    rank += (cu > cs) || (cu == cs && u < s);
   }
-  if (s < n) order[rank] = s;
+  rank = (int)__reduce_add_sync(0xffffffffu, (unsigned)rank);
+  if (lane == 0) order[rank] = s;
 }
 
 struct __align__(64) SelBwdParams {
@@ -152,28 +149,49 @@ struct __align__(64) SelBwdParams {
   float scale;
 };
 
-// D_r = sum_e dO_re O_re (f32).  One warp per query row, 4 elements per lane.
+// D_r = sum_e dO_re O_re (f32).  Half a warp per query row, 16 bytes per lane,
+// 4 rows in flight per half warp: bound by reading o and dout once.
+constexpr int kSelPrepRows = 64;  // per CTA of 256 threads
 __global__ void __launch_bounds__(256)
     select_prep_kernel(const __grid_constant__ SelBwdParams p) {
   const long long rows = (long long)p.B * p.Hq * p.Lq;
-  const long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
-  const uint2 a = reinterpret_cast<const uint2*>(p.o + row * kBwdD)[lane];
-  const uint2 g = reinterpret_cast<const uint2*>(p.dout + row * kBwdD)[lane];
-  float s = bf16lo(a.x) * bf16lo(g.x) + bf16hi(a.x) * bf16hi(g.x) +
-            bf16lo(a.y) * bf16lo(g.y) + bf16hi(a.y) * bf16hi(g.y);
+  const int sub = threadIdx.x & 15;
+  const long long row0 =
+      (long long)blockIdx.x * kSelPrepRows + (threadIdx.x >> 4);
+  uint4 a[4], g[4];
 #pragma unroll
-  for (int m = 16; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-  if (lane == 0) {
-    const long long r = row / p.Lq, q = row - r * p.Lq;
-    p.delta[r * p.Lqp + q] = s;
-    p.lse2[r * p.Lqp + q] = p.lse[row] * kPrefLog2e;
-    if (q == p.Lq - 1)  // the row's padding columns: finite, never used
-      for (int c = p.Lq; c < p.Lqp; ++c) {
-        p.delta[r * p.Lqp + c] = 0.f;
-        p.lse2[r * p.Lqp + c] = 0.f;
-      }
+  for (int i = 0; i < 4; ++i) {
+    const long long row = row0 + 16 * i;
+    if (row < rows) {
+      a[i] = __ldg(reinterpret_cast<const uint4*>(p.o + row * kBwdD) + sub);
+      g[i] = __ldg(reinterpret_cast<const uint4*>(p.dout + row * kBwdD) + sub);
+    } else {
+      a[i] = g[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const long long row = row0 + 16 * i;
+    const uint32_t x[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+    const uint32_t y[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+    float s = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s = fmaf(bf16lo(x[e]), bf16lo(y[e]), s);
+      s = fmaf(bf16hi(x[e]), bf16hi(y[e]), s);
+    }
+#pragma unroll
+    for (int m = 8; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+    if (sub == 0 && row < rows) {
+      const long long r = row / p.Lq, q = row - r * p.Lq;
+      p.delta[r * p.Lqp + q] = s;
+      p.lse2[r * p.Lqp + q] = p.lse[row] * kPrefLog2e;
+      if (q == p.Lq - 1)  // the row's padding columns: finite, never used
+        for (int c = p.Lq; c < p.Lqp; ++c) {
+          p.delta[r * p.Lqp + c] = 0.f;
+          p.lse2[r * p.Lqp + c] = 0.f;
+        }
+    }
   }
 }
 
@@ -925,7 +943,8 @@ inline cudaError_t launch_select_backward(const SelBwdProblem& pr,
   const long long planes = (long long)pr.B * pr.Hq;
   const long long slots = (long long)BH * nk;
   const long long tiles = (long long)BH * gm.ntile;
-  const long long prep_blocks = (long long)((rows + 7) / 8);
+  const long long prep_blocks =
+      (long long)((rows + kSelPrepRows - 1) / kSelPrepRows);
   if (prep_blocks > 0x7fffffffLL || slots > 0x7fffffffLL ||
       tiles > 0x7fffffffLL)
     return cudaErrorInvalidConfiguration;
@@ -998,7 +1017,7 @@ inline cudaError_t launch_select_backward(const SelBwdProblem& pr,
   if (e != cudaSuccess) return e;
   if (slots <= kBwdOrderMaxSlots) {  // (the rank is quadratic)
     int* order = reinterpret_cast<int*>(ws + w.order);
-    select_order_kernel<<<(unsigned)((slots + 255) / 256), 256, 0, st>>>(
+    select_order_kernel<<<(unsigned)((slots + 7) / 8), 256, 0, st>>>(
         a.count, (int)slots, order);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
