@@ -296,42 +296,66 @@ struct RowTask {
 };
 
 // The same cut for R rows of one warp whose n <= 32 NR finite scores fit its
-// registers: t splits off exactly k (split), or equal values at t straddle
-// the cut.  A prompt has a row per token and KV head, so this sets the
-// selection's time: about 9 bisection steps of NR compares and one warp
-// reduction, two rows interleaved to cover each other's latency.
+// registers: t splits off exactly k (split), or equal values at t (or a float
+// step above it) straddle the cut.  A prompt has a row per token and KV head,
+// so this sets the selection's time.  The first thresholds come from the
+// normal distribution of the scores' mean and variance (a score sums d
+// products) and from its density there, the next from bisection: about 4
+// passes of NR compares and one warp reduction where bisection alone takes 9.
+// Two rows are interleaved to cover each other's latency.
 template <int NR, int R>
 __device__ __forceinline__ void find_cuts(const RowTask (&r)[R],
                                           float (&v)[R][NR], float (&t)[R],
                                           bool (&split)[R]) {
   const int lane = threadIdx.x & 31;
-  float lo[R], hi[R], mx[R];
+  // at least k values are >= lo; fewer than k are >= hi, or hi is the maximum
+  float lo[R], hi[R], gain[R];
   bool live[R];
 #pragma unroll
   for (int y = 0; y < R; ++y) {
-    mx[y] = -INFINITY;
+    hi[y] = -INFINITY;
     lo[y] = INFINITY;
+    float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int x = 0; x < NR; ++x) {
       const int i = 32 * x + lane;
-      v[y][x] = i < r[y].n ? r[y].s[i] : -INFINITY;
-      mx[y] = fmaxf(mx[y], v[y][x]);
-      lo[y] = fminf(lo[y], i < r[y].n ? v[y][x] : INFINITY);
+      const bool in = i < r[y].n;
+      v[y][x] = in ? r[y].s[i] : -INFINITY;
+      hi[y] = fmaxf(hi[y], v[y][x]);
+      lo[y] = fminf(lo[y], in ? v[y][x] : INFINITY);
+      const float z = in ? v[y][x] : 0.f;
+      s1 += z;
+      s2 = fmaf(z, z, s2);
+    }
+    hi[y] = redux_max(hi[y]);
+    lo[y] = redux_min(lo[y]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      s1 += __shfl_xor_sync(~0u, s1, o);
+      s2 += __shfl_xor_sync(~0u, s2, o);
+    }
+    // the k / n quantile of a normal distribution (Abramowitz and Stegun,
+    // 26.2.22: within 3e-3) and 1 / (n times its density there)
+    const float n = (float)r[y].n;
+    const float mu = s1 / n, sd = sqrtf(fmaxf(s2 / n - mu * mu, 0.f));
+    const float p = (float)r[y].k / n, q = fminf(p, 1.f - p);
+    const float w = sqrtf(-2.f * __logf(q));
+    float z = w - __fdividef(2.30753f + 0.27061f * w,
+                             1.f + w * (0.99229f + 0.04481f * w));
+    gain[y] = __fdividef(2.5066283f * sd, n) * __expf(0.5f * z * z);
+    t[y] = p < 0.5f ? fmaf(z, sd, mu) : fmaf(-z, sd, mu);
+    split[y] = false;
+    live[y] = lo[y] < hi[y];
+    if (!(t[y] > lo[y] && t[y] < hi[y])) t[y] = 0.5f * lo[y] + 0.5f * hi[y];
+    if (!(t[y] > lo[y])) {  // one value, or two with no float between
+      t[y] = lo[y];
+      live[y] = false;
     }
   }
-  // at least k values are >= lo; fewer than k are >= hi, or hi is untried:
-  // the first threshold tried is the maximum
+  bool any = false;
 #pragma unroll
-  for (int y = 0; y < R; ++y) {
-    mx[y] = redux_max(mx[y]);
-    lo[y] = redux_min(lo[y]);
-    hi[y] = mx[y];
-    t[y] = mx[y];
-    split[y] = false;
-    live[y] = true;
-  }
-  bool any = true;
-  while (any) {
+  for (int y = 0; y < R; ++y) any = any || live[y];
+  for (int pass = 0; any; ++pass) {
     int c[R];
 #pragma unroll
     for (int y = 0; y < R; ++y) {
@@ -346,21 +370,23 @@ __device__ __forceinline__ void find_cuts(const RowTask (&r)[R],
 #pragma unroll
     for (int y = 0; y < R; ++y) {
       if (!live[y]) continue;
-      if (c[y] == r[y].k) {
+      const int d = c[y] - r[y].k;
+      if (d == 0) {
         split[y] = true;
         live[y] = false;
         continue;
       }
-      if (c[y] > r[y].k) lo[y] = t[y];
+      if (d > 0) lo[y] = t[y];
       else hi[y] = t[y];
-      const float m = 0.5f * lo[y] + 0.5f * hi[y];
-      // equal values straddle the cut: at the maximum, or between neighbours
-      if (lo[y] == mx[y] || !(m > lo[y] && m < hi[y])) {
-        t[y] = lo[y];
-        live[y] = false;
-      } else {
+      float m = fmaf((float)d, gain[y], t[y]);
+      if (pass >= 3 || !(m > lo[y] && m < hi[y]))
+        m = 0.5f * lo[y] + 0.5f * hi[y];
+      if (m > lo[y] && m < hi[y]) {
         t[y] = m;
         any = true;
+      } else {
+        t[y] = lo[y];
+        live[y] = false;
       }
     }
   }
@@ -368,9 +394,10 @@ __device__ __forceinline__ void find_cuts(const RowTask (&r)[R],
 
 // The take of one row after its cut.  When the cut is not wider than 2 eps,
 // the blocks within 2 eps of it (2 or 3, on a few rows of a hundred) get a
-// lane each for their float64 score and are ranked there.  Returns false, with
-// nothing written, when they are more than 32, or when equal scores straddle
-// the cut and eps is 0.
+// lane each for their float64 score and are ranked there.  (Without a split
+// the equal values lie within a float step of t, far inside 2 eps.)  Returns
+// false, with nothing written, when they are more than 32, or when equal
+// scores straddle the cut and eps is 0.
 template <int NR, class ExactT>
 __device__ __forceinline__ bool take_cut(const RowTask& r, const float (&v)[NR],
                                          float t, bool split, ExactT exact) {
@@ -558,24 +585,27 @@ __device__ __forceinline__ bool fill_fixed(GroupT& g, const SelRange& r,
   return !all && mid > 0;
 }
 
-// Relative error bounds of the float32 scores, against |sum_g |q_g|| |c|.
-// Tensor core: splitting the head sum into two bf16 parts loses 2^-16 of it,
-// its float32 sum G 2^-24 <= 2^-19 (G <= 32), and the accumulation of d/8
-// steps of 16 products about 2^-18: below 2^-15.  CUDA cores (no split): the
-// head sum 2^-19, 13 roundings of 2^-24 in the dot product: below 2^-18.
-constexpr float kSelEpsMma = 3.0517578125e-05f;   // 2^-15
+// Error bounds of the float32 scores: |w| |c| (2-norms), w the error of each
+// term of the dot product per unit of c.
+// Tensor core: x = sum_g q_g is split into two bf16 parts, whose rest is known
+// exactly; its float32 sum is off by (G - 1) 2^-24 sum_g |q_g|; accumulating
+// 2 d / 16 steps of 16 products takes 2^-17 |x|.
+// CUDA cores (no split): the head sum 2^-19 sum_g |q_g| for G <= 32, and 13
+// roundings of 2^-24 in the dot product: below 2^-18 sum_g |q_g|.
+constexpr float kSelEpsMma = 7.62939453125e-06f;   // 2^-17
 constexpr float kSelEpsFma = 3.814697265625e-06f;  // 2^-18
-// Norms are summed over values scaled by 2^40, so that squares of small
+// Norms of q are summed over values scaled by 2^40, so that squares of small
 // values stay above float32's smallest (a sum that overflows only sends the
 // row to the float64 scores).
 constexpr float kNormUp = 1099511627776.f, kNormDown = 1.f / 1099511627776.f;
 
-// The error bound of a row whose |sum_g |q_g|| is nq, against means of norm
-// at most nc.  The product is formed first: where it overflows, so may the
-// scores, and the bound has to be infinite.
-__device__ __forceinline__ float score_eps(float rel, float nq, float nc) {
-  const float e = rel * (nq * nc);
-  return nq > 0.f && nc > 0.f ? fmaxf(e, 1e-37f) : e;
+// nw nc, for the norm nw of w and the largest norm nc of a mean; infinite
+// where the scores themselves may leave float32's range (w is at least 2^-18
+// of what they sum).
+__device__ __forceinline__ float score_eps(float nw, float nc) {
+  const float e = nw * nc;
+  if (!(e < 1e33f)) return INFINITY;
+  return nw > 0.f && nc > 0.f ? fmaxf(e, 1e-37f) : 0.f;
 }
 
 // The float64 score of one block for the whole warp; qd holds the lane's
@@ -698,7 +728,7 @@ __global__ void __launch_bounds__(kSelDecThreads, 2)
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) qq += __shfl_xor_sync(~0u, qq, o);
-    eps = score_eps(kSelEpsFma, sqrtf(qq) * kNormDown,
+    eps = score_eps(kSelEpsFma * (sqrtf(qq) * kNormDown),
                     sqrtf(__uint_as_float(cmax_s)) * kNormDown);
   }
   double qd[D / 32];
@@ -793,7 +823,7 @@ struct SelectCfg {
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_C = OFF_Q + TM * QROW;       // [2][64][D] bf16
   static constexpr int CBYTES = kSelBlock * D * 2;
-  static constexpr int OFF_N = OFF_C + 2 * CBYTES;      // f32 [TM] |q| bound
+  static constexpr int OFF_N = OFF_C + 2 * CBYTES;      // f32 [TM] |w|
   static constexpr int OFF_CM = OFF_N + TM * 4;
   static constexpr int OFF_S = (OFF_CM + 4 + 127) / 128 * 128;
   static constexpr int smem(int ld) { return OFF_S + TM * ld * 4; }
@@ -844,6 +874,7 @@ __global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
   {
     const __nv_bfloat16* q0 =
         a.q + ((size_t)b * a.Hkv + h) * (size_t)a.G * a.Lq * D;
+    const float head_eps = (float)(a.G - 1) * 5.9604644775390625e-08f;  // 2^-24
     for (int e = tid; e < TM * CH; e += 256) {
       const int row = e / CH, ch = e % CH;
       float x[8], y[8];
@@ -874,8 +905,17 @@ __global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
         ph[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
         pl[i] = pack_bf16x2(x[2 * i] - bf16lo(ph[i]),
                             x[2 * i + 1] - bf16hi(ph[i]));
-        nn = fmaf(y[2 * i] * kNormUp, y[2 * i] * kNormUp, nn);
-        nn = fmaf(y[2 * i + 1] * kNormUp, y[2 * i + 1] * kNormUp, nn);
+        // the error of these two columns, see kSelEpsMma
+        const float w0 = fmaf(kSelEpsMma, fabsf(x[2 * i]),
+                              fmaf(head_eps, y[2 * i],
+                                   fabsf(x[2 * i] - bf16lo(ph[i]) - bf16lo(pl[i])))) *
+                         kNormUp;
+        const float w1 = fmaf(kSelEpsMma, fabsf(x[2 * i + 1]),
+                              fmaf(head_eps, y[2 * i + 1],
+                                   fabsf(x[2 * i + 1] - bf16hi(ph[i]) - bf16hi(pl[i])))) *
+                         kNormUp;
+        nn = fmaf(w0, w0, nn);
+        nn = fmaf(w1, w1, nn);
       }
       uint8_t* dst = sq + row * C::QROW;
       *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) << 4)) =
@@ -944,29 +984,30 @@ __global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
       *reinterpret_cast<float2*>(S + (size_t)(row + 8) * a.ld + col) =
           make_float2(acc[nt][2], acc[nt][3]);
     }
-    // the largest |c|^2 among the tile's blocks
-    float cm = 0.f;
-    for (int e = tid; e < kSelBlock * CH; e += 256) {
-      const int row = e / CH, ch = e % CH;
-      const uint4 w = *reinterpret_cast<const uint4*>(
-          cb + row * (D * 2) + ((ch ^ (row & 7)) << 4));
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-      float nn = 0.f;
+    // The largest |c|^2 among the tile's blocks: the diagonal of c c^T, 8
+    // blocks a warp (a row-major A fragment of 8 rows is their B fragment).
+    float d0 = 0.f, d1 = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float lo = bf16lo(ww[i]), hi = bf16hi(ww[i]);
-        nn = fmaf(lo * kNormUp, lo * kNormUp, nn);
-        nn = fmaf(hi * kNormUp, hi * kNormUp, nn);
-      }
-#pragma unroll
-      for (int o = CH / 2; o; o >>= 1) nn += __shfl_xor_sync(~0u, nn, o);
-      cm = __uint_as_float(max(__float_as_uint(cm), __float_as_uint(fabsf(nn))));
+    for (int p = 0; p < KST / 2; ++p) {
+      const int row = warp * 8 + mr;
+      uint32_t r0, r1, r2, r3;
+      ldsm_x4(ca + row * (D * 2) + (((4 * p + mi) ^ (row & 7)) << 4), r0, r1, r2,
+              r3);
+      mma16816_top(d0, d1, r0, r1, r0, r1);
+      mma16816_top(d0, d1, r2, r3, r2, r3);
     }
-    const uint32_t cw = __reduce_max_sync(~0u, __float_as_uint(cm));
+    // lane: row lane / 4, columns 2 (lane % 4) and the next
+    const float nn = (lane >> 2) == 2 * (lane & 3)       ? d0
+                     : (lane >> 2) == 2 * (lane & 3) + 1 ? d1
+                                                         : 0.f;
+    const uint32_t cw = __reduce_max_sync(~0u, __float_as_uint(fabsf(nn)));
     if (lane == 0) atomicMax(cmax_s, cw);
     __syncthreads();
   }
-  const float cmax = sqrtf(__uint_as_float(*cmax_s)) * kNormDown;
+  // (squares below float32's smallest normal number lose their digits: no
+  // norm counts as less than 2e-18 unless it is 0; NaN stays NaN)
+  float cmax = sqrtf(__uint_as_float(*cmax_s));
+  if (*cmax_s != 0u && cmax < 2e-18f) cmax = 2e-18f;
   WarpGroup g;
   // two rows at a time
   for (int rr = 2 * warp; rr < nrow; rr += 16) {
@@ -981,7 +1022,7 @@ __global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
       int* out = a.sel + ((size_t)bh * a.Lq + row) * a.n_sel;
       todo[y] = rr + y < nrow && fill_fixed(g, r, a.n_sel, out);
       task[y] = {S + (size_t)(row - row0) * a.ld + r.f, out + r.f, r.f,
-                 r.m1 - r.f, r.k, score_eps(kSelEpsMma, nrm[row - row0], cmax)};
+                 r.m1 - r.f, r.k, score_eps(nrm[row - row0], cmax)};
       if (todo[y]) nmax = max(nmax, task[y].n);
     }
     if (!todo[0] && !todo[1]) continue;
