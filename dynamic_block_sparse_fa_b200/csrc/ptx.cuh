@@ -336,6 +336,25 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
+// Two fused multiply-adds (two additions) in one instruction (sm_100):
+// (d0, d1) = (a0, a1) * b + c;  (d0, d1) += (a0, a1).
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1,
+                                     float b, float c) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\t"
+      "mov.b64 z, {%5, %5};\n\tfma.rn.f32x2 x, x, y, z;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
+  asm("{\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%0, %1};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1));
+}
+
 // bf16x2 word -> two floats (exact: a bf16 is the top half of an f32).
 __device__ __forceinline__ float bf16lo(uint32_t w) {
   return __uint_as_float(w << 16);

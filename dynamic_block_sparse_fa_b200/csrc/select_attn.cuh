@@ -350,6 +350,9 @@ __global__ void __launch_bounds__(352, 1)
     float2* xm = reinterpret_cast<float2*>(smem + C::OFF_XM) + rr;
     float2* xl = reinterpret_cast<float2*>(smem + C::OFF_XL) + rr;
 
+    // The chunk of exps after which the row's max and reference go over: the
+    // other group's exps follow this group's.
+    constexpr int kTurn = 2;
     float m_ref = -INFINITY;  // reference of l (scaled, natural units)
     float l = 0.f;            // of this group's steps
     bool ok = true;
@@ -419,6 +422,12 @@ __global__ void __launch_bounds__(352, 1)
         mt = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
                    fmaxf(m8[6], m8[7]));
       }
+      if (s >= 2) {  // the P buffer is free: this group's last P.V is over
+        w = mbar_wait(&bar[C::B_OF + grp], par ^ 1, kWaitSelect, s, 425);
+        ok = __all_sync(FULL, w);
+        if (!ok) break;
+        tc_fence_after();
+      }
       // the row's running max and reference after step s - 1
       float2 m = make_float2(-INFINITY, -INFINITY);
       if (s > 0) {
@@ -438,8 +447,6 @@ __global__ void __launch_bounds__(352, 1)
       }
       // (free: the other group's step s - 1 read it before it wrote its own)
       xm[grp * 128] = m;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[C::B_MX + grp * 4 + quad]);
       if (m.y != m_ref) {  // the reference moved since this group's last step
         l *= m_ref == -INFINITY ? 0.f : ex2_approx((m_ref - m.y) * kPrefLog2e);
         m_ref = m.y;
@@ -451,19 +458,20 @@ __global__ void __launch_bounds__(352, 1)
         uint32_t pk[16];
 #pragma unroll
         for (int x = 0; x < 32; x += 2) {
-          const float p0 = ex2_approx(fmaf(__uint_as_float(sr[c][x]), sl2, mb));
-          const float p1 = ex2_approx(fmaf(__uint_as_float(sr[c][x + 1]), sl2, mb));
-          rs[(x >> 1) & 3] += p0 + p1;
-          pk[x / 2] = pack_bf16x2(p0, p1);
-        }
-        if (c == 0 && s >= 2) {  // the P buffer: this group's last P.V is over
-          w = mbar_wait(&bar[C::B_OF + grp], par ^ 1, kWaitSelect, s, 425);
-          ok = __all_sync(FULL, w);
-          tc_fence_after();
+          float a0, a1;
+          fma2(a0, a1, __uint_as_float(sr[c][x]), __uint_as_float(sr[c][x + 1]),
+               sl2, mb);
+          a0 = ex2_approx(a0);
+          a1 = ex2_approx(a1);
+          add2(rs[x & 2], rs[(x & 2) + 1], a0, a1);
+          pk[x / 2] = pack_bf16x2(a0, a1);
         }
         tmem_st16(lane_base + col_p + c * 16, pk);
+        if (c == kTurn) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar[C::B_MX + grp * 4 + quad]);
+        }
       }
-      if (!ok) break;
       l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
       if (s > 0 && __any_sync(FULL, rescale)) {
         // O is idle once P.V of step s - 1 is complete (the step before it
