@@ -347,6 +347,26 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1,
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b), "f"(c));
 }
+// (d0, d1) = (a0, a1) * b + (c0, c1);  (a0, a1) + (c0, c1);  products.
+__device__ __forceinline__ void fma2v(float& d0, float& d1, float a0, float a1,
+                                      float b, float c0, float c1) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %4};\n\t"
+      "mov.b64 z, {%5, %6};\n\tfma.rn.f32x2 x, x, y, z;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
+}
+// (d0, d1) = (p0, p1) * ((a0, a1) + (c0, c1))
+__device__ __forceinline__ void add_mul2(float& d0, float& d1, float p0, float p1,
+                                         float a0, float a1, float c0, float c1) {
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "mov.b64 y, {%2, %3};\n\tadd.rn.f32x2 x, x, z;\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(p0), "f"(p1), "f"(a0), "f"(a1), "f"(c0), "f"(c1));
+}
 __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
   asm("{\n\t.reg .b64 x, y;\n\t"
       "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%0, %1};\n\t"

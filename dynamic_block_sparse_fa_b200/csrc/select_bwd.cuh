@@ -19,7 +19,7 @@
 // a third fewer than the 128-key pairs.  Both passes sum in a fixed order.
 //
 // Before them:
-//   select_prep_kernel   D and lse * log2 e per query row
+//   select_prep_kernel   -D and -lse * log2 e per query row
 //   select_lists_kernel  per tile: its blocks and their token bits
 //   select_bits_kernel   per (KV head, tile): the token bits of every block,
 //                        stored block-major
@@ -125,12 +125,12 @@ __global__ void __launch_bounds__(256)
 struct __align__(64) SelBwdParams {
   CUtensorMap tq, tdo;        // query tiles (TQ tokens x G heads)
   CUtensorMap tk, tv;         // box 64 rows
-  CUtensorMap tdel, tlse2;    // those rows' D and lse * log2 e
+  CUtensorMap tdel, tlse2;    // those rows' -D and -lse * log2 e
   const __nv_bfloat16* o;     // [B, Hq, Lq, D]
   const __nv_bfloat16* dout;  // [B, Hq, Lq, D]
   const float* lse;           // [B, Hq, Lq] natural log
-  float* delta;               // [B*Hq][Lqp]
-  float* lse2;                // [B*Hq][Lqp]
+  float* delta;               // [B*Hq][Lqp] -D
+  float* lse2;                // [B*Hq][Lqp] -lse * log2 e
   __nv_bfloat16* dq;          // [B, Hq, Lq, D]
   __nv_bfloat16* dk;          // [B, Hkv, Lkv, D]
   __nv_bfloat16* dv;          // [B, Hkv, Lkv, D]
@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(256)
     for (int m = 8; m >= 1; m >>= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
     if (sub == 0 && row < rows) {
       const long long r = row / p.Lq, q = row - r * p.Lq;
-      p.delta[r * p.Lqp + q] = s;
-      p.lse2[r * p.Lqp + q] = p.lse[row] * kPrefLog2e;
+      p.delta[r * p.Lqp + q] = -s;
+      p.lse2[r * p.Lqp + q] = -p.lse[row] * kPrefLog2e;
       if (q == p.Lq - 1)  // the row's padding columns: finite, never used
         for (int c = p.Lq; c < p.Lqp; ++c) {
           p.delta[r * p.Lqp + c] = 0.f;
@@ -454,10 +454,15 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
 #pragma unroll
           for (int x = 0; x < 32; x += 4) {
             const float4 l4 = lse4[u * 8 + (x >> 2)];
-            const float p0 = ex2_approx(fmaf(__uint_as_float(sv[x]), sl2, -l4.x));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(sv[x + 1]), sl2, -l4.y));
-            const float p2 = ex2_approx(fmaf(__uint_as_float(sv[x + 2]), sl2, -l4.z));
-            const float p3 = ex2_approx(fmaf(__uint_as_float(sv[x + 3]), sl2, -l4.w));
+            float p0, p1, p2, p3;
+            fma2v(p0, p1, __uint_as_float(sv[x]), __uint_as_float(sv[x + 1]),
+                  sl2, l4.x, l4.y);
+            fma2v(p2, p3, __uint_as_float(sv[x + 2]), __uint_as_float(sv[x + 3]),
+                  sl2, l4.z, l4.w);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            p2 = ex2_approx(p2);
+            p3 = ex2_approx(p3);
             st[x >> 1] = pack_bf16x2(p0, p1);
             st[(x >> 1) + 1] = pack_bf16x2(p2, p3);
             pk[u * 16 + (x >> 1)] = pack_f16x2(p0, p1);
@@ -467,13 +472,14 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
 #pragma unroll
           for (int x = 0; x < 32; x += 4) {
             const float4 l4 = lse4[u * 8 + (x >> 2)];
-            const float ll[4] = {l4.x, l4.y, l4.z, l4.w};
             float pv[4];
+            fma2v(pv[0], pv[1], __uint_as_float(sv[x]), __uint_as_float(sv[x + 1]),
+                  sl2, l4.x, l4.y);
+            fma2v(pv[2], pv[3], __uint_as_float(sv[x + 2]),
+                  __uint_as_float(sv[x + 3]), sl2, l4.z, l4.w);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              pv[e] = (cm[u] >> (x + e)) & 1u
-                          ? ex2_approx(fmaf(__uint_as_float(sv[x + e]), sl2, -ll[e]))
-                          : 0.f;
+              pv[e] = (cm[u] >> (x + e)) & 1u ? ex2_approx(pv[e]) : 0.f;
             st[x >> 1] = pack_bf16x2(pv[0], pv[1]);
             st[(x >> 1) + 1] = pack_bf16x2(pv[2], pv[3]);
             pk[u * 16 + (x >> 1)] = pack_f16x2(pv[0], pv[1]);
@@ -501,11 +507,13 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
           const float4 d4 = del4[u * 8 + (x >> 2)];
           const float2 pa = unpack_f16x2(pk[u * 16 + (x >> 1)]);
           const float2 pb = unpack_f16x2(pk[u * 16 + (x >> 1) + 1]);
-          st[x >> 1] = pack_bf16x2(pa.x * (__uint_as_float(dp[x]) - d4.x),
-                                   pa.y * (__uint_as_float(dp[x + 1]) - d4.y));
-          st[(x >> 1) + 1] =
-              pack_bf16x2(pb.x * (__uint_as_float(dp[x + 2]) - d4.z),
-                          pb.y * (__uint_as_float(dp[x + 3]) - d4.w));
+          float s0, s1, s2, s3;
+          add_mul2(s0, s1, pa.x, pa.y, __uint_as_float(dp[x]),
+                   __uint_as_float(dp[x + 1]), d4.x, d4.y);
+          add_mul2(s2, s3, pb.x, pb.y, __uint_as_float(dp[x + 2]),
+                   __uint_as_float(dp[x + 3]), d4.z, d4.w);
+          st[x >> 1] = pack_bf16x2(s0, s1);
+          st[(x >> 1) + 1] = pack_bf16x2(s2, s3);
         }
         tmem_st16(lane_base + 128 + u * 16, st);
       }
@@ -767,8 +775,8 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
         p.words + (slot * p.cap + h) * (size_t)p.wpt + (tt >> 5);
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     const float sl2 = p.scale * kPrefLog2e;
-    const float del = active ? __ldg(p.delta + (size_t)(zq + g) * p.Lqp + tok) : 0.f;
-    const float nl2 = active ? -__ldg(p.lse2 + (size_t)(zq + g) * p.Lqp + tok) : 0.f;
+    const float ndel = active ? __ldg(p.delta + (size_t)(zq + g) * p.Lqp + tok) : 0.f;
+    const float nl2 = active ? __ldg(p.lse2 + (size_t)(zq + g) * p.Lqp + tok) : 0.f;
     bool ok = true;
     uint2 e_n = make_uint2(0, 0);
     unsigned w_n = 0;
@@ -802,9 +810,14 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float e = ex2_approx(fmaf(__uint_as_float(sv[c][x]), sl2, nl2));
-          sv[c][x] = on ? __float_as_uint(e) : 0u;
+        for (int x = 0; x < 32; x += 2) {
+          float e0, e1;
+          fma2(e0, e1, __uint_as_float(sv[c][x]), __uint_as_float(sv[c][x + 1]),
+               sl2, nl2);
+          e0 = ex2_approx(e0);
+          e1 = ex2_approx(e1);
+          sv[c][x] = on ? __float_as_uint(e0) : 0u;
+          sv[c][x + 1] = on ? __float_as_uint(e1) : 0u;
         }
       if (!plain) {
 #pragma unroll
@@ -825,10 +838,13 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
         tmem_ld32(lane_base + 128 + h * 64 + c * 32, dp);
         tc_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 32; x += 2)
-          st[x >> 1] = pack_bf16x2(
-              __uint_as_float(sv[c][x]) * (__uint_as_float(dp[x]) - del),
-              __uint_as_float(sv[c][x + 1]) * (__uint_as_float(dp[x + 1]) - del));
+        for (int x = 0; x < 32; x += 2) {
+          float s0, s1;
+          add_mul2(s0, s1, __uint_as_float(sv[c][x]),
+                   __uint_as_float(sv[c][x + 1]), __uint_as_float(dp[x]),
+                   __uint_as_float(dp[x + 1]), ndel, ndel);
+          st[x >> 1] = pack_bf16x2(s0, s1);
+        }
         tmem_st16(lane_base + 384 + (s & 1) * 64 + h * 32 + c * 16, st);
       }
       tc_wait_st();
