@@ -10,6 +10,7 @@ raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -735,11 +736,10 @@ def _disjoint(outs, ins):
                 raise ValueError(f"{name} overlaps {other}")
 
 
-def _launch(name, dev, stream, *args):
-    """Calls the C entry point on the tensors' device and the given stream
-    (default: that device's current one)."""
-    raw = (torch._C._cuda_getCurrentRawStream(dev) if stream is None
-           else stream.cuda_stream)
+def _launch(name, dev, *args):
+    """Calls the C entry point on the tensors' device and that device's
+    current stream."""
+    raw = torch._C._cuda_getCurrentRawStream(dev)
     if torch._C._cuda_getDevice() == dev:
         st = getattr(_lib, name)(*args, raw)
     else:
@@ -770,7 +770,20 @@ def _pool(k_pages, v_pages=None):
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
-def blasst_block_means(k, *, means=None, stream=None):
+def _on_stream(fn):
+    """stream=s runs the call as under torch.cuda.stream(s): what it allocates
+    (outputs, workspace) then belongs to that stream too."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+@_on_stream
+def blasst_block_means(k, *, means=None):
     """Mean of every 64-key block: k [B,Hkv,L,d] bf16 -> [B,Hkv,nblk,d]."""
     B, Hkv, L, d = k.shape
     dev = _device(k, "k")
@@ -779,14 +792,15 @@ def blasst_block_means(k, *, means=None, stream=None):
         means = k.new_empty(shape)
     else:
         _disjoint([("means", means)], [("k", k)])
-    _launch("blasst_block_means", dev, stream,
+    _launch("blasst_block_means", dev,
             _addr(k, "k", _BF16, None, dev),
             _addr(means, "means", _BF16, shape, dev), B, Hkv, L, d)
     return means
 
 
+@_on_stream
 def blasst_block_means_paged(k_pages, block_table, seq_lens, means, *,
-                             max_seq_len=None, n_new=0, stream=None):
+                             max_seq_len=None, n_new=0):
     """Bring ``means`` [B,Hkv,max_blocks,d] (updated in place and returned) up
     to date with a paged cache: the blocks that hold the last ``n_new`` tokens
     of each sequence, or every block for n_new = 0.  Pool, table and lengths
@@ -800,7 +814,7 @@ def blasst_block_means_paged(k_pages, block_table, seq_lens, means, *,
         max_seq_len = min(mp * ps, nb * SELECT_BLOCK)
     _disjoint([("means", means)], [("block_table", block_table),
                                    ("seq_lens", seq_lens)])
-    _launch("blasst_block_means_paged", dev, stream,
+    _launch("blasst_block_means_paged", dev,
             _addr(k_pages, "k_pages", _BF16, None, dev, False), stride, P, ps,
             _addr(block_table, "block_table", _I32, None, dev), mp,
             _addr(seq_lens, "seq_lens", _I32, (B,), dev), int(max_seq_len),
@@ -809,8 +823,9 @@ def blasst_block_means_paged(k_pages, block_table, seq_lens, means, *,
     return means
 
 
+@_on_stream
 def blasst_block_select(q, means, Lkv, *, n_sel, n_first=1, n_local=1,
-                        causal=True, sel=None, stream=None):
+                        causal=True, sel=None):
     """The n_sel key blocks every row of q [B,Hq,Lq,d] attends to, from the
     block means [B,Hkv,nblk,d] of its Lkv keys: int32 [B,Hkv,Lq,n_sel],
     ascending, -1 in unused slots.  The first n_first and the last n_local
@@ -823,7 +838,7 @@ def blasst_block_select(q, means, Lkv, *, n_sel, n_first=1, n_local=1,
         sel = q.new_empty(shape, dtype=_I32)
     else:
         _disjoint([("sel", sel)], [("q", q), ("means", means)])
-    _launch("blasst_block_select", dev, stream,
+    _launch("blasst_block_select", dev,
             _addr(q, "q", _BF16, None, dev),
             _addr(means, "means", _BF16, (B, Hkv, _nblk(Lkv), d), dev),
             _addr(sel, "sel", _I32, shape, dev), B, Hq, Hkv, Lq, int(Lkv), d,
@@ -831,9 +846,9 @@ def blasst_block_select(q, means, Lkv, *, n_sel, n_first=1, n_local=1,
     return sel
 
 
+@_on_stream
 def blasst_block_select_decode(q, means, seq_lens, *, n_sel, n_first=1,
-                               n_local=1, max_seq_len=None, sel=None,
-                               stream=None):
+                               n_local=1, max_seq_len=None, sel=None):
     """blasst_block_select for one token per sequence: q [B,Hq,d], means
     [B,Hkv,max_blocks,d], seq_lens [B] int32 -> int32 [B,Hkv,n_sel]."""
     B, Hq, d = q.shape
@@ -847,7 +862,7 @@ def blasst_block_select_decode(q, means, seq_lens, *, n_sel, n_first=1,
                                    ("seq_lens", seq_lens)])
     if max_seq_len is None:
         max_seq_len = nb * SELECT_BLOCK
-    _launch("blasst_block_select_decode", dev, stream,
+    _launch("blasst_block_select_decode", dev,
             _addr(q, "q", _BF16, None, dev),
             _addr(means, "means", _BF16, (B, Hkv, nb, d), dev),
             _addr(seq_lens, "seq_lens", _I32, (B,), dev), int(max_seq_len), nb,
@@ -877,9 +892,9 @@ def _workspace(workspace, need, like):
     return like.new_empty(max(need, 1), dtype=torch.uint8)
 
 
+@_on_stream
 def blasst_select_prefill(q, k, v, sel, *, scale=None, causal=True, o=None,
-                          lse=None, want_lse=True, workspace=None,
-                          stream=None):
+                          lse=None, want_lse=True, workspace=None):
     """Attention over the selected key blocks.  q [B,Hq,Lq,d], k/v
     [B,Hkv,Lkv,d] bf16, sel [B,Hkv,Lq,n_sel] int32 block ids (any order, -1
     for none).  Returns (o, lse)."""
@@ -899,7 +914,7 @@ def blasst_select_prefill(q, k, v, sel, *, scale=None, causal=True, o=None,
         lse = q.new_empty((B, Hq, Lq), dtype=_F32)
     ws = _workspace(workspace, _lib.blasst_select_prefill_workspace_size(
         B, Hq, Hkv, Lq, Lkv), q)
-    _launch("blasst_select_prefill", dev, stream,
+    _launch("blasst_select_prefill", dev,
             _addr(q, "q", _BF16, None, dev),
             _addr(k, "k", _BF16, (B, Hkv, Lkv, d), dev),
             _addr(v, "v", _BF16, (B, Hkv, Lkv, d), dev),
@@ -912,9 +927,10 @@ def blasst_select_prefill(q, k, v, sel, *, scale=None, causal=True, o=None,
     return o, lse
 
 
+@_on_stream
 def blasst_select_prefill_backward(q, k, v, o, lse, dout, sel, *, scale=None,
                                    causal=True, dq=None, dk=None, dv=None,
-                                   workspace=None, stream=None):
+                                   workspace=None):
     """Gradients (dq, dk, dv) of a blasst_select_prefill forward with its
     selection held fixed (d = 128); o and lse are that forward's."""
     B, Hq, Lq, d = q.shape
@@ -935,7 +951,7 @@ def blasst_select_prefill_backward(q, k, v, o, lse, dout, sel, *, scale=None,
                     _lib.blasst_select_prefill_backward_workspace_size(
                         B, Hq, Hkv, Lq, Lkv, d), q)
     qs, ks = q.shape, (B, Hkv, Lkv, d)
-    _launch("blasst_select_prefill_backward", dev, stream,
+    _launch("blasst_select_prefill_backward", dev,
             _addr(q, "q", _BF16, None, dev), _addr(k, "k", _BF16, ks, dev),
             _addr(v, "v", _BF16, ks, dev), _addr(o, "o", _BF16, qs, dev),
             _addr(dout, "dout", _BF16, qs, dev),
@@ -949,10 +965,10 @@ def blasst_select_prefill_backward(q, k, v, o, lse, dout, sel, *, scale=None,
     return dq, dk, dv
 
 
+@_on_stream
 def blasst_select_decode_paged(q, k_pages, v_pages, block_table, seq_lens, sel,
                                *, max_seq_len=None, scale=None, num_splits=0,
-                               o=None, lse=None, want_lse=True, workspace=None,
-                               stream=None):
+                               o=None, lse=None, want_lse=True, workspace=None):
     """One token per sequence over the selected blocks of a paged cache:
     arguments as blasst_decode_paged, sel [B,Hkv,n_sel] int32 block ids (any
     order, -1 for none).  Returns (o, lse).  Bad lengths, page ids and block
@@ -981,7 +997,7 @@ def blasst_select_decode_paged(q, k_pages, v_pages, block_table, seq_lens, sel,
          else _lib.blasst_select_decode_splits(B, Hq, Hkv, n_sel))
     ws = _workspace(workspace, _lib.blasst_decode_workspace_size(B, Hq, d, S),
                     q)
-    _launch("blasst_select_decode_paged", dev, stream,
+    _launch("blasst_select_decode_paged", dev,
             _addr(q, "q", _BF16, None, dev),
             _addr(k_pages, "k_pages", _BF16, None, dev, False),
             _addr(v_pages, "v_pages", _BF16, None, dev, False), stride, P, ps,

@@ -129,6 +129,21 @@ struct __align__(64) SelPrefillParams {
   int causal;
 };
 
+// Waits for the last loads of a ring of n slots into which `issued` loads went
+// in order.  After a run without failures every one has been waited for.
+__device__ __forceinline__ void drain_ring(uint64_t* full, int n, int issued) {
+  for (int u = issued > n ? issued - n : 0; u < issued; ++u)
+    mbar_wait(&full[u % n], (uint32_t)(u / n) & 1u, kWaitSelect, u, 900);
+}
+// Waits, after some other wait gave up, for the products issued so far (whole
+// warp): tensor memory is freed and operands are released behind this.
+__device__ __forceinline__ void drain_mma(uint64_t* bar) {
+  __syncwarp();
+  mma_commit_elect(bar);
+  mbar_wait(bar, 0, kWaitSelect, 0, 901);
+  __syncwarp();
+}
+
 template <int D>
 struct SelPrefillCfg {
   static constexpr int NKS = 3, NVS = 2;
@@ -153,7 +168,8 @@ struct SelPrefillCfg {
   static constexpr int B_PR = B_SR + 2;    // P written, O scaled (per warp)
   static constexpr int B_OF = B_PR + 2;    // P.V complete
   static constexpr int B_MX = B_OF + 2;    // [2][4 quadrants] maxima written
-  static constexpr int NBAR = B_MX + 8;
+  static constexpr int B_DR = B_MX + 8;    // drain after a wait gave up
+  static constexpr int NBAR = B_DR + 1;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_TMEM + 8;
   static constexpr int SMEM_ALLOC = SMEM + 1024;
@@ -212,6 +228,7 @@ __global__ void __launch_bounds__(352, 1)
       mbar_init(&bar[C::B_OF + i], 1);
     }
     for (int i = 0; i < 8; ++i) mbar_init(&bar[C::B_MX + i], 1);
+    mbar_init(&bar[C::B_DR], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -246,9 +263,9 @@ __global__ void __launch_bounds__(352, 1)
                       tile * p.TQ, zq, pol_q);
       }
       uint2 next = __ldg(list);
-      int sl = 0;
+      int sl = 0, s = 0;
       uint32_t par = 1;  // of the slot's previous use
-      for (int s = 0; s < ns; ++s) {
+      for (; s < ns; ++s) {
         const uint2 e = next;
         if (s + 1 < ns) next = __ldg(list + s + 1);
         if (s >= nslot &&
@@ -268,6 +285,9 @@ __global__ void __launch_bounds__(352, 1)
           par ^= 1;
         }
       }
+      // no copy is left in flight, whatever became of its readers
+      drain_ring(full, nslot, s);
+      if (is_k) mbar_wait(&bar[C::B_Q], 0, kWaitSelect, s, 402);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -326,6 +346,7 @@ __global__ void __launch_bounds__(352, 1)
         mma_commit_elect(&bar[C::B_OF + vs]);
         mma_commit_elect(&bar[C::B_VE + vs]);
       }
+      if (!ok) drain_mma(&bar[C::B_DR]);
     }
     __syncwarp();
   } else {

@@ -225,7 +225,8 @@ struct SelDkdvCfg {
   static constexpr int B_PR = 7;   // P^T written (one arrival per warp)
   static constexpr int B_DSR = 8;  // dS^T written (one arrival per warp)
   static constexpr int B_OD = 9;   // every product complete
-  static constexpr int NBAR = 10;
+  static constexpr int B_DR = 10;  // drain after a wait gave up
+  static constexpr int NBAR = 11;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_TMEM + 8;
   static constexpr int SMEM_ALLOC = SMEM + 1024;
@@ -265,6 +266,7 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
     mbar_init(&bar[C::B_PR], 8);
     mbar_init(&bar[C::B_DSR], 8);
     mbar_init(&bar[C::B_OD], 1);
+    mbar_init(&bar[C::B_DR], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -292,8 +294,8 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
           tma_load_3d(smem + C::OFF_V + at, &p.tv, &bar[C::B_KV], c * 64,
                       jb * 128 + h * 64, bk, pol_kv);
         }
-      int next = __ldg(tlist);
-      for (int n = 0; n < nt; ++n) {
+      int next = __ldg(tlist), n = 0;
+      for (; n < nt; ++n) {
         const int r0 = next * p.TQ;
         if (n + 1 < nt) next = __ldg(tlist + n + 1);
         const int s = n & 1;
@@ -314,6 +316,9 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
         tma_load_3d(smem + C::OFF_DEL + s * 512, &p.tdel, &bar[C::B_QF + s],
                     r0, zq, 0, pol_q);
       }
+      // no copy is left in flight, whatever became of its readers
+      drain_ring(&bar[C::B_QF], 2, n);
+      mbar_wait(&bar[C::B_KV], 0, kWaitSelect, n, 502);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -384,7 +389,10 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
           mma_commit_elect(&bar[C::B_DPF]);
         }
       }
-      if (ok) mma_commit_elect(&bar[C::B_OD]);
+      if (ok)
+        mma_commit_elect(&bar[C::B_OD]);
+      else
+        drain_mma(&bar[C::B_DR]);
     }
     __syncwarp();
   } else {
@@ -596,7 +604,8 @@ struct SelDqCfg {
   static constexpr int B_DPF = B_SR + 1;   // dP in TMEM
   static constexpr int B_DSR = B_DPF + 1;  // dS written (one per warp)
   static constexpr int B_OD = B_DSR + 1;
-  static constexpr int NBAR = B_OD + 1;
+  static constexpr int B_DR = B_OD + 1;    // drain after a wait gave up
+  static constexpr int NBAR = B_DR + 1;
   static constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
   static constexpr int SMEM = OFF_TMEM + 8;
   static constexpr int SMEM_ALLOC = SMEM + 1024;
@@ -640,6 +649,7 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
     mbar_init(&bar[C::B_DPF], 1);
     mbar_init(&bar[C::B_DSR], 8);
     mbar_init(&bar[C::B_OD], 1);
+    mbar_init(&bar[C::B_DR], 1);
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -676,6 +686,7 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
         }
       };
       uint2 next = __ldg(list);
+      int nk = 0, nv = 0;  // loads issued
       for (int s = 0; s < ns; ++s) {
         const uint2 e = next;
         if (s + 1 < ns) next = __ldg(list + s + 1);
@@ -684,11 +695,17 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
                                       kWaitSelect, s, 530))
           break;
         load(&p.tk, smem + C::OFF_K + ks * C::TILE, &bar[C::B_KF + ks], e);
+        ++nk;
         if (s >= C::NVS && !mbar_wait(&bar[C::B_VE + vs], (s / C::NVS - 1) & 1,
                                       kWaitSelect, s, 531))
           break;
         load(&p.tv, smem + C::OFF_V + vs * C::TILE, &bar[C::B_VF + vs], e);
+        ++nv;
       }
+      // no copy is left in flight, whatever became of its readers
+      drain_ring(&bar[C::B_KF], C::NKS, nk);
+      drain_ring(&bar[C::B_VF], C::NVS, nv);
+      mbar_wait(&bar[C::B_Q], 0, kWaitSelect, nk, 532);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -757,7 +774,10 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
         mma_commit_elect(&bar[C::B_KE + k0]);
         k0 = k1;
       }
-      if (ok) mma_commit_elect(&bar[C::B_OD]);
+      if (ok)
+        mma_commit_elect(&bar[C::B_OD]);
+      else
+        drain_mma(&bar[C::B_DR]);
     }
     __syncwarp();
   } else {

@@ -630,9 +630,10 @@ blasst_status_t blasst_select_prefill(const void *q, const void *k,
  *  d = 128; other limits as the forward
  *  workspace  blasst_select_prefill_backward_workspace_size() bytes, 256-byte
  *             aligned, caller-owned
- * dQ is summed over key blocks in float32 by atomic additions, so its last
- * bits depend on their order.  Asynchronous on `stream`; five or six kernel
- * launches; allocates nothing.
+ * Each gradient is summed in float32 in a fixed order.  P and dS are rounded
+ * to bf16 for their tensor-core products, and D = dO . O uses the bf16 o.
+ * Asynchronous on `stream`; seven kernel launches (six when B * Hkv *
+ * ceil(Lkv/128) exceeds 32768); allocates nothing.
  */
 size_t blasst_select_prefill_backward_workspace_size(int B, int Hq, int Hkv,
                                                      int Lq, int Lkv, int d);

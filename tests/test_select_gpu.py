@@ -746,3 +746,111 @@ def test_binding_refuses(m):
     with pytest.raises(m.BlasstError):
         m.blasst_select_prefill(q, k, v, sel, workspace=torch.empty(
             16, dtype=torch.uint8, device="cuda"))
+
+
+# ------------------------------------------------- what one might trip over
+def test_results_are_the_same_bits_every_run(m):
+    g = _gen(80)
+    q, k, v = _qkv(g, 2, 8, 2, 900, 900, 128)
+    do = _rand(g, 2, 8, 900, 128)
+    a = _chain_prompt(m, q, k, v, do, 6)
+    b = _chain_prompt(m, q, k, v, do, 6)
+    _clean(m)
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+
+
+def test_stream_argument(m):
+    """stream=s runs there; its workspace is not handed to the current stream
+    while the call still uses it."""
+    g = _gen(81)
+    q, k, v = _qkv(g, 1, 8, 2, 2000, 2000, 128)
+    do = _rand(g, 1, 8, 2000, 128)
+    sel = R.random_selection(torch.Generator().manual_seed(8), 1, 2, 2000, 2000,
+                             5, True, "cuda")
+    o, lse = m.blasst_select_prefill(q, k, v, sel)
+    want = m.blasst_select_prefill_backward(q, k, v, o, lse, do, sel)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        o2, lse2 = m.blasst_select_prefill(q, k, v, sel, stream=s)
+        got = m.blasst_select_prefill_backward(q, k, v, o2, lse2, do, sel,
+                                               stream=s)
+        for _ in range(4):       # the current stream allocates and overwrites
+            torch.empty(1 << 24, dtype=torch.uint8, device="cuda").fill_(255)
+    torch.cuda.synchronize()
+    _clean(m)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+
+
+def test_offsets_past_32_bits(m):
+    """Keys behind element 2^31 (contiguous), and pages behind element 2^32."""
+    L = (1 << 31) // (2 * 128) + 1000
+    k = torch.empty(1, 3, L, 128, dtype=BF, device="cuda")
+    g = _gen(82)
+    tail = _rand(g, 1000, 128)
+    k[0, 2, -1000:] = tail
+    c = m.blasst_block_means(k)
+    nb = R.nblk(L)
+    first = -(-(L - 1000) // 64)
+    n = L - first * 64
+    _check_means(c[0, 2, first:], R.means(tail[-n:]), tail.abs().max().item())
+    del k, c
+    P, H, ps, d = 40, 2, 64, 128
+    stride = 1 << 27
+    pool = torch.empty((P - 1) * stride + 2 * H * ps * d, dtype=BF,
+                       device="cuda")
+    pages = pool.as_strided((P, 2, H, ps, d),
+                            (stride, H * ps * d, ps * d, d, 1))
+    ids = [39, 33, 1, 38]
+    kv = _rand(g, 2, H, 4 * ps, d)
+    for i, x in enumerate(ids):
+        pages[x] = kv[:, :, i * ps:(i + 1) * ps]
+    bt = torch.tensor([ids], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([250], dtype=torch.int32, device="cuda")
+    means = torch.zeros(1, H, 4, d, dtype=BF, device="cuda")
+    m.blasst_block_means_paged(pages[:, 0], bt, lens, means)
+    _check_means(means[0], R.means(kv[0, :, :250]), kv.abs().max().item())
+    q = _rand(g, 1, 8, d)
+    sel = m.blasst_block_select_decode(q, means, lens, n_sel=3)
+    o, lse = m.blasst_select_decode_paged(q, pages[:, 0], pages[:, 1], bt, lens,
+                                          sel)
+    _clean(m)
+    _check_o(o, R.decode(q, kv[:1], kv[1:], sel, [250], 1 / math.sqrt(d)), lse)
+
+
+@pytest.mark.parametrize("L", [64 * 250, 64 * 700, 64 * 1500, 64 * 4000])
+def test_select_decode_lengths(m, L):
+    """One warp's registers, and beyond them the whole CTA; near ties that
+    only the exact score resolves among them."""
+    g = _gen(L)
+    nb = L // 64
+    q = _rand(g, 2, 8, 128)
+    c = _rand(g, 2, 2, nb, 128)
+    c[1] = c[1, :, :1]
+    at = torch.randint(0, 128, (nb,), generator=g, device="cuda")
+    c[1, :, torch.arange(nb, device="cuda"), at] *= 1 + 2.0 ** -7
+    lens = torch.tensor([L, L], dtype=torch.int32, device="cuda")
+    got = m.blasst_block_select_decode(q, c, lens, n_sel=50, n_local=2)
+    _clean(m)
+    for b in range(2):
+        for h in range(2):
+            ref = R.select(q[b, h * 4:(h + 1) * 4, None].cpu(), c[b, h].cpu(),
+                           [nb - 1], 50, 1, 2)[0]
+            assert torch.equal(got[b, h].cpu(), ref), (b, h)
+
+
+def test_select_scores_as_large_as_their_bound(m):
+    """Queries along the means: the products of a score all have one sign, and
+    the best scores crowd together."""
+    g = _gen(84)
+    base = _rand(g, 128).float()
+    c = (base + 0.02 * torch.randn(1, 1, 300, 128, generator=g,
+                                   device="cuda")).to(BF)
+    q = (base + 0.02 * torch.randn(1, 4, 96, 128, generator=g,
+                                   device="cuda")).to(BF)
+    got = m.blasst_block_select(q, c, 19200, n_sel=40, causal=False)
+    _clean(m)
+    assert torch.equal(got.cpu(), _ref_select(q, c, 19200, False, 40, 1, 1))
