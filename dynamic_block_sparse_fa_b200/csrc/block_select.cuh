@@ -789,12 +789,15 @@ cudaError_t launch_block_select_decode(const SelectArgs& a, int B, int nblk,
 }
 
 // ---------------------------------------------------------------------------
-// Every row of a prompt: a CTA of 8 warps takes TM rows of one KV head.  The
+// Every row of a prompt: a CTA of 8 warps takes 16 rows of one KV head.  The
 // head sums are split into two bf16 parts (16 bits of each sum) and scored
 // against the means on the tensor core (mma.sync: 2 d deep, far from its
 // limit, and the scores land in registers, one shared-memory store away from
-// the selection); all scores of the TM rows stay in shared memory, then each
-// warp selects for its rows.
+// the selection); all scores of the rows stay in shared memory, then each warp
+// selects for two of them.  What bounds it is the selection's instructions,
+// so what counts is warps to hide their latency: 16 rows take 57 KB at 16K
+// keys, three CTAs per SM (215 us for 32 heads on 8 at 16K; 32 rows, two CTAs,
+// 223; 64 rows, one, 336.  B 2, 777 rows on 5K keys: 12.1, 19.8, 19.8).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4],
                                          uint32_t b0, uint32_t b1) {
@@ -817,8 +820,11 @@ __device__ __forceinline__ void cp_async_wait_but_one() {
   asm volatile("cp.async.wait_group 1;" ::: "memory");
 }
 
-template <int D, int TM>
+constexpr int kSelRows = 16;  // rows per CTA
+
+template <int D>
 struct SelectCfg {
+  static constexpr int TM = kSelRows;
   static constexpr int QROW = 2 * D * 2;  // hi and lo halves of a row, bytes
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_C = OFF_Q + TM * QROW;       // [2][64][D] bf16
@@ -829,14 +835,13 @@ struct SelectCfg {
   static constexpr int smem(int ld) { return OFF_S + TM * ld * 4; }
 };
 
-template <int D, int TM>
-__global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
-  using C = SelectCfg<D, TM>;
+template <int D>
+__global__ void __launch_bounds__(256, 3)
+    block_select_kernel(const SelectArgs a) {
+  using C = SelectCfg<D>;
+  constexpr int TM = kSelRows;
   constexpr int CH = D / 8;
   constexpr int KST = D / 16;
-  constexpr int WM = TM / 16;       // warps along the rows
-  constexpr int WN = 8 / WM;        // warps along the blocks
-  constexpr int NT = kSelBlock / WN / 8;
   extern __shared__ __align__(128) uint8_t sel_raw[];
   uint8_t* sq = sel_raw + C::OFF_Q;
   uint8_t* sc = sel_raw + C::OFF_C;
@@ -928,11 +933,11 @@ __global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
     }
   }
   __syncthreads();
-  const int wm = warp % WM, wn = warp / WM;
+  // each warp scores all rows against 8 of a tile's 64 blocks
   const int mi = lane >> 3, mr = lane & 7;
   uint32_t ah[KST][4], al[KST][4];
   {
-    const int row = 16 * wm + (mi & 1) * 8 + mr;
+    const int row = (mi & 1) * 8 + mr;
     const uint32_t base = smem_u32(sq) + row * C::QROW;
 #pragma unroll
     for (int ks = 0; ks < KST; ++ks) {
@@ -951,50 +956,33 @@ __global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
       cp_async_wait_all();
     }
     __syncthreads();
-    const uint8_t* cb = sc + (ct & 1) * C::CBYTES;
-    const uint32_t ca = smem_u32(cb);
-    float acc[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) acc[nt][x] = 0.f;
-#pragma unroll
-    for (int p = 0; p < KST / 2; ++p) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int row = wn * (NT * 8) + nt * 8 + mr;
-        uint32_t r0, r1, r2, r3;
-        ldsm_x4(ca + row * (D * 2) + (((4 * p + mi) ^ (row & 7)) << 4), r0, r1,
-                r2, r3);
-        mma16816(acc[nt], ah[2 * p], r0, r1);
-        mma16816(acc[nt], al[2 * p], r0, r1);
-        mma16816(acc[nt], ah[2 * p + 1], r2, r3);
-        mma16816(acc[nt], al[2 * p + 1], r2, r3);
-      }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int col = ct * kSelBlock + wn * (NT * 8) + nt * 8 + 2 * (lane & 3);
-      const int row = 16 * wm + (lane >> 2);
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (isnan(acc[nt][x])) acc[nt][x] = -INFINITY;
-      *reinterpret_cast<float2*>(S + (size_t)row * a.ld + col) =
-          make_float2(acc[nt][0], acc[nt][1]);
-      *reinterpret_cast<float2*>(S + (size_t)(row + 8) * a.ld + col) =
-          make_float2(acc[nt][2], acc[nt][3]);
-    }
-    // The largest |c|^2 among the tile's blocks: the diagonal of c c^T, 8
-    // blocks a warp (a row-major A fragment of 8 rows is their B fragment).
-    float d0 = 0.f, d1 = 0.f;
+    const uint32_t ca = smem_u32(sc + (ct & 1) * C::CBYTES);
+    // The scores, and the largest |c|^2 among the tile's blocks: the diagonal
+    // of c c^T (a row-major A fragment of 8 rows is their B fragment).
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, d0 = 0.f, d1 = 0.f;
 #pragma unroll
     for (int p = 0; p < KST / 2; ++p) {
       const int row = warp * 8 + mr;
       uint32_t r0, r1, r2, r3;
       ldsm_x4(ca + row * (D * 2) + (((4 * p + mi) ^ (row & 7)) << 4), r0, r1, r2,
               r3);
+      mma16816(acc, ah[2 * p], r0, r1);
+      mma16816(acc, al[2 * p], r0, r1);
+      mma16816(acc, ah[2 * p + 1], r2, r3);
+      mma16816(acc, al[2 * p + 1], r2, r3);
       mma16816_top(d0, d1, r0, r1, r0, r1);
       mma16816_top(d0, d1, r2, r3, r2, r3);
+    }
+    {
+      const int col = ct * kSelBlock + warp * 8 + 2 * (lane & 3);
+      const int row = lane >> 2;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (isnan(acc[x])) acc[x] = -INFINITY;
+      *reinterpret_cast<float2*>(S + (size_t)row * a.ld + col) =
+          make_float2(acc[0], acc[1]);
+      *reinterpret_cast<float2*>(S + (size_t)(row + 8) * a.ld + col) =
+          make_float2(acc[2], acc[3]);
     }
     // lane: row lane / 4, columns 2 (lane % 4) and the next
     const float nn = (lane >> 2) == 2 * (lane & 3)       ? d0
@@ -1079,35 +1067,23 @@ __global__ void __launch_bounds__(256) block_select_kernel(const SelectArgs a) {
   }
 }
 
-template <int D, int TM>
-cudaError_t launch_block_select_t(const SelectArgs& a0, int B,
-                                  cudaStream_t st) {
-  SelectArgs a = a0;
-  a.ntile = (a.Lq + TM - 1) / TM;
-  const int smem = SelectCfg<D, TM>::smem(a.ld);
-  const long long grid = (long long)a.ntile * B * a.Hkv;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(
-      block_select_kernel<D, TM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      smem);
-  if (e != cudaSuccess) return e;
-  block_select_kernel<D, TM><<<(unsigned)grid, 256, smem, st>>>(a);
-  return cudaGetLastError();
-}
-
-// Score columns a prompt tile keeps: whole 64-block tiles, plus 8 floats so
-// that the 8 rows a fragment store writes fall into different banks.
+// Score columns kept per row: whole 64-block tiles, plus 8 floats so that the 8
+// rows a fragment store writes fall into different banks.
 inline int select_ld(int nblk) { return (nblk + 63) / 64 * 64 + 8; }
 
 template <int D>
 cudaError_t launch_block_select(SelectArgs a, int B, cudaStream_t st) {
   a.ld = select_ld(a.nblk);
-  constexpr int kTwo = 113 * 1024;  // two CTAs per SM
-  if (SelectCfg<D, 64>::smem(a.ld) <= kTwo)
-    return launch_block_select_t<D, 64>(a, B, st);
-  if (SelectCfg<D, 32>::smem(a.ld) <= kTwo)
-    return launch_block_select_t<D, 32>(a, B, st);
-  return launch_block_select_t<D, 16>(a, B, st);
+  a.ntile = (a.Lq + kSelRows - 1) / kSelRows;
+  const int smem = SelectCfg<D>::smem(a.ld);
+  const long long grid = (long long)a.ntile * B * a.Hkv;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(
+      block_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      smem);
+  if (e != cudaSuccess) return e;
+  block_select_kernel<D><<<(unsigned)grid, 256, smem, st>>>(a);
+  return cudaGetLastError();
 }
 
 }  // namespace blasst
