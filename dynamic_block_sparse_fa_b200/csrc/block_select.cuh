@@ -295,100 +295,64 @@ struct RowTask {
   float eps;
 };
 
-// The same cut for R rows of one warp whose n <= 32 NR finite scores fit its
-// registers: t splits off exactly k (split), or equal values at t (or a float
-// step above it) straddle the cut.  A prompt has a row per token and KV head,
-// so this sets the selection's time.  The first thresholds come from the
-// normal distribution of the scores' mean and variance (a score sums d
-// products) and from its density there, the next from bisection: about 4
-// passes of NR compares and one warp reduction where bisection alone takes 9.
-// Two rows are interleaved to cover each other's latency.
-template <int NR, int R>
-__device__ __forceinline__ void find_cuts(const RowTask (&r)[R],
-                                          float (&v)[R][NR], float (&t)[R],
-                                          bool (&split)[R]) {
+// The same cut for one warp whose n <= 32 NR finite scores fit its registers:
+// t splits off exactly k (split), or equal values at t (or a float step above
+// it) straddle the cut.  A prompt has a row per token and KV head, so this
+// sets the selection's time.  The first thresholds come from the normal
+// distribution of the scores' mean and variance (a score sums d products) and
+// from its density there, the next from bisection: about 4 passes of NR
+// compares and one warp reduction where bisection alone takes 9.
+template <int NR>
+__device__ __forceinline__ void find_cut(const RowTask& r, float (&v)[NR],
+                                         float& t, bool& split) {
   const int lane = threadIdx.x & 31;
   // at least k values are >= lo; fewer than k are >= hi, or hi is the maximum
-  float lo[R], hi[R], gain[R];
-  bool live[R];
+  float lo = INFINITY, hi = -INFINITY, s1 = 0.f, s2 = 0.f;
 #pragma unroll
-  for (int y = 0; y < R; ++y) {
-    hi[y] = -INFINITY;
-    lo[y] = INFINITY;
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      const int i = 32 * x + lane;
-      const bool in = i < r[y].n;
-      v[y][x] = in ? r[y].s[i] : -INFINITY;
-      hi[y] = fmaxf(hi[y], v[y][x]);
-      lo[y] = fminf(lo[y], in ? v[y][x] : INFINITY);
-      const float z = in ? v[y][x] : 0.f;
-      s1 += z;
-      s2 = fmaf(z, z, s2);
-    }
-    hi[y] = redux_max(hi[y]);
-    lo[y] = redux_min(lo[y]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      s1 += __shfl_xor_sync(~0u, s1, o);
-      s2 += __shfl_xor_sync(~0u, s2, o);
-    }
-    // the k / n quantile of a normal distribution (Abramowitz and Stegun,
-    // 26.2.22: within 3e-3) and 1 / (n times its density there)
-    const float n = (float)r[y].n;
-    const float mu = s1 / n, sd = sqrtf(fmaxf(s2 / n - mu * mu, 0.f));
-    const float p = (float)r[y].k / n, q = fminf(p, 1.f - p);
-    const float w = sqrtf(-2.f * __logf(q));
-    float z = w - __fdividef(2.30753f + 0.27061f * w,
-                             1.f + w * (0.99229f + 0.04481f * w));
-    gain[y] = __fdividef(2.5066283f * sd, n) * __expf(0.5f * z * z);
-    t[y] = p < 0.5f ? fmaf(z, sd, mu) : fmaf(-z, sd, mu);
-    split[y] = false;
-    live[y] = lo[y] < hi[y];
-    if (!(t[y] > lo[y] && t[y] < hi[y])) t[y] = 0.5f * lo[y] + 0.5f * hi[y];
-    if (!(t[y] > lo[y])) {  // one value, or two with no float between
-      t[y] = lo[y];
-      live[y] = false;
-    }
+  for (int x = 0; x < NR; ++x) {
+    const int i = 32 * x + lane;
+    const bool in = i < r.n;
+    v[x] = in ? r.s[i] : -INFINITY;
+    hi = fmaxf(hi, v[x]);
+    lo = fminf(lo, in ? v[x] : INFINITY);
+    const float z = in ? v[x] : 0.f;
+    s1 += z;
+    s2 = fmaf(z, z, s2);
   }
-  bool any = false;
+  hi = redux_max(hi);
+  lo = redux_min(lo);
 #pragma unroll
-  for (int y = 0; y < R; ++y) any = any || live[y];
-  for (int pass = 0; any; ++pass) {
-    int c[R];
+  for (int o = 16; o; o >>= 1) {
+    s1 += __shfl_xor_sync(~0u, s1, o);
+    s2 += __shfl_xor_sync(~0u, s2, o);
+  }
+  // the k / n quantile of a normal distribution (Abramowitz and Stegun,
+  // 26.2.22: within 3e-3) and 1 / (n times its density there)
+  const float n = (float)r.n;
+  const float mu = s1 / n, sd = sqrtf(fmaxf(s2 / n - mu * mu, 0.f));
+  const float p = (float)r.k / n, q = fminf(p, 1.f - p);
+  const float w = sqrtf(-2.f * __logf(q));
+  const float z = w - __fdividef(2.30753f + 0.27061f * w,
+                                 1.f + w * (0.99229f + 0.04481f * w));
+  const float gain = __fdividef(2.5066283f * sd, n) * __expf(0.5f * z * z);
+  t = p < 0.5f ? fmaf(z, sd, mu) : fmaf(-z, sd, mu);
+  split = false;
+  if (!(t > lo && t < hi)) t = 0.5f * lo + 0.5f * hi;
+  if (!(t > lo && t < hi)) t = lo;  // one value, or no float between two
+  for (int pass = 0; t > lo; ++pass) {
+    int c = 0;
 #pragma unroll
-    for (int y = 0; y < R; ++y) {
-      c[y] = 0;
-#pragma unroll
-      for (int x = 0; x < NR; ++x) c[y] += v[y][x] >= t[y];
+    for (int x = 0; x < NR; ++x) c += v[x] >= t;
+    const int d = (int)__reduce_add_sync(~0u, (unsigned)c) - r.k;
+    if (d == 0) {
+      split = true;
+      return;
     }
-#pragma unroll
-    for (int y = 0; y < R; ++y)
-      c[y] = (int)__reduce_add_sync(~0u, (unsigned)c[y]);
-    any = false;
-#pragma unroll
-    for (int y = 0; y < R; ++y) {
-      if (!live[y]) continue;
-      const int d = c[y] - r[y].k;
-      if (d == 0) {
-        split[y] = true;
-        live[y] = false;
-        continue;
-      }
-      if (d > 0) lo[y] = t[y];
-      else hi[y] = t[y];
-      float m = fmaf((float)d, gain[y], t[y]);
-      if (pass >= 3 || !(m > lo[y] && m < hi[y]))
-        m = 0.5f * lo[y] + 0.5f * hi[y];
-      if (m > lo[y] && m < hi[y]) {
-        t[y] = m;
-        any = true;
-      } else {
-        t[y] = lo[y];
-        live[y] = false;
-      }
-    }
+    if (d > 0) lo = t;
+    else hi = t;
+    t = fmaf((float)d, gain, t);
+    if (pass >= 3 || !(t > lo && t < hi)) t = 0.5f * lo + 0.5f * hi;
+    if (!(t > lo && t < hi)) t = lo;
   }
 }
 
@@ -474,6 +438,15 @@ __device__ __forceinline__ bool take_cut(const RowTask& r, const float (&v)[NR],
   return true;
 }
 
+// Cut and take of one row whose n <= 32 NR; false: left to take_general.
+template <int NR, class ExactT>
+__device__ __forceinline__ bool take_row(const RowTask& r, ExactT exact) {
+  float v[NR], t;
+  bool split;
+  find_cut<NR>(r, v, t, split);
+  return take_cut<NR>(r, v, t, split, exact);
+}
+
 // The take of one row in general, by a warp or a CTA, for any n: s is
 // overwritten where the cut needs it.  exact(j) (taken by a whole warp) is the
 // float64 score of block j.
@@ -537,11 +510,6 @@ __device__ void take_general(GroupT& g, float* s, const RowTask& r,
     out += total;
   }
 }
-
-template <int N>
-struct IntTag {
-  static constexpr int value = N;
-};
 
 struct SelectArgs {
   const __nv_bfloat16* q;      // [B, Hq, Lq, d]; decode [B, Hq, d]
@@ -755,17 +723,9 @@ __global__ void __launch_bounds__(kSelDecThreads, 2)
     WarpGroup wg;
     bool todo = fill_fixed(wg, r, a.n_sel, out);
     if (todo && eps < INFINITY) {
-      auto fast = [&](auto nr_tag) {
-        constexpr int NR = decltype(nr_tag)::value;
-        const RowTask rt[1] = {task};
-        float v[1][NR], t[1];
-        bool split[1];
-        find_cuts<NR, 1>(rt, v, t, split);
-        todo = !take_cut<NR>(task, v[0], t[0], split[0], exact);
-      };
-      if (n <= 256) fast(IntTag<8>());
-      else if (n <= 512) fast(IntTag<16>());
-      else if (n <= 1024) fast(IntTag<32>());
+      if (n <= 256) todo = !take_row<8>(task, exact);
+      else if (n <= 512) todo = !take_row<16>(task, exact);
+      else if (n <= 1024) todo = !take_row<32>(task, exact);
     }
     if (lane == 0) by_cta = todo;
   }
@@ -997,31 +957,23 @@ __global__ void __launch_bounds__(256, 3)
   float cmax = sqrtf(__uint_as_float(*cmax_s));
   if (*cmax_s != 0u && cmax < 2e-18f) cmax = 2e-18f;
   WarpGroup g;
-  // two rows at a time
-  for (int rr = 2 * warp; rr < nrow; rr += 16) {
-    RowTask task[2];
-    bool todo[2];
-    int nmax = 0;
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-      const int row = row0 + min(rr + y, nrow - 1);
-      const int last = (a.causal ? row + off : a.Lkv - 1) / kSelBlock;
-      const SelRange r = sel_range(last, a.n_sel, a.n_first, a.n_local);
-      int* out = a.sel + ((size_t)bh * a.Lq + row) * a.n_sel;
-      todo[y] = rr + y < nrow && fill_fixed(g, r, a.n_sel, out);
-      task[y] = {S + (size_t)(row - row0) * a.ld + r.f, out + r.f, r.f,
-                 r.m1 - r.f, r.k, score_eps(nrm[row - row0], cmax)};
-      if (todo[y]) nmax = max(nmax, task[y].n);
-    }
-    if (!todo[0] && !todo[1]) continue;
-    // the float64 score of block j for row y
+  for (int rr = warp; rr < nrow; rr += 8) {
+    const int row = row0 + rr;
+    const int last = (a.causal ? row + off : a.Lkv - 1) / kSelBlock;
+    const SelRange r = sel_range(last, a.n_sel, a.n_first, a.n_local);
+    int* out = a.sel + ((size_t)bh * a.Lq + row) * a.n_sel;
+    if (!fill_fixed(g, r, a.n_sel, out)) continue;
+    float* srow = S + (size_t)rr * a.ld + r.f;
+    const RowTask task = {srow, out + r.f, r.f, r.m1 - r.f, r.k,
+                          score_eps(nrm[rr], cmax)};
+    // the float64 score of block j
     double qd[D / 32];
-    int have = -1;
-    auto exact = [&](int y, int j) {
-      if (have != y) {
-        have = y;
+    bool have_q = false;
+    auto exact = [&](int j) {
+      if (!have_q) {
+        have_q = true;
         const __nv_bfloat16* q =
-            a.q + (((size_t)b * a.Hkv + h) * a.G * (size_t)a.Lq + row0 + rr + y) * D;
+            a.q + (((size_t)b * a.Hkv + h) * a.G * (size_t)a.Lq + row) * D;
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) qd[x] = 0.0;
         for (int gg = 0; gg < a.G; ++gg)
@@ -1032,37 +984,14 @@ __global__ void __launch_bounds__(256, 3)
       }
       return exact_score<D>(qd, c0 + (size_t)j * D);
     };
-    // rows the register path cannot take stay to do
-    auto fast = [&](auto nr_tag) {
-      constexpr int NR = decltype(nr_tag)::value;
-      float v[2][NR], t[2];
-      bool split[2];
-      RowTask rt[2];
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        rt[y] = task[y];
-        if (!todo[y]) rt[y] = task[y ^ 1];  // (a finished row shadows the other)
-      }
-      find_cuts<NR, 2>(rt, v, t, split);
-#pragma unroll
-      for (int y = 0; y < 2; ++y)
-        if (todo[y])
-          todo[y] = !take_cut<NR>(task[y], v[y], t[y], split[y],
-                                  [&](int j) { return exact(y, j); });
-    };
-    if ((!todo[0] || task[0].eps < INFINITY) &&
-        (!todo[1] || task[1].eps < INFINITY)) {
-      if (nmax <= 64) fast(IntTag<2>());
-      else if (nmax <= 128) fast(IntTag<4>());
-      else if (nmax <= 256) fast(IntTag<8>());
-      else if (nmax <= 512) fast(IntTag<16>());
+    bool todo = true;
+    if (task.eps < INFINITY) {
+      if (task.n <= 64) todo = !take_row<2>(task, exact);
+      else if (task.n <= 128) todo = !take_row<4>(task, exact);
+      else if (task.n <= 256) todo = !take_row<8>(task, exact);
+      else if (task.n <= 512) todo = !take_row<16>(task, exact);
     }
-#pragma unroll 1
-    for (int y = 0; y < 2; ++y) {
-      if (!todo[y]) continue;
-      const RowTask rt = y ? task[1] : task[0];
-      take_general(g, S + (rt.s - S), rt, [&](int j) { return exact(y, j); });
-    }
+    if (todo) take_general(g, srow, task, exact);
     __syncwarp();
   }
 }
