@@ -13,7 +13,7 @@
 //
 // select_lists_kernel turns the selection into, per tile, the ascending list
 // of blocks any of its tokens selected and, per listed block, one bit per
-// token.  select_prefill_kernel (a TMA producer warp, an MMA issuer warp, 8
+// token (for the backward also the bits of all blocks, block-major).  select_prefill_kernel (a TMA producer warp, an MMA issuer warp, 8
 // softmax warps) walks that list two blocks (128 keys) a step.
 #pragma once
 
@@ -45,8 +45,10 @@ struct SelListArgs {
   int* nstep;       // [B*Hkv*ntile]
   unsigned* list;   // [B*Hkv*ntile][cap] block ids
   unsigned* words;  // [B*Hkv*ntile][cap][wpt]
+  unsigned* bits;   // backward: [B*Hkv][nblk2][ntile][wpt], block-major
   int Lq, Lkv, n_sel, causal;
   int TQ, wpt, ntile, nblk, cap;
+  int nblk2;        // nblk rounded up to whole 128 keys
 };
 
 // Sets the bits of the selection rows [row0, row0 + nrow) in shared words
@@ -55,18 +57,21 @@ __device__ __forceinline__ void sel_set_bits(const int* sel, unsigned* bits,
                                              int W, int row0, int nrow,
                                              int n_sel, int off, int causal,
                                              int nblk, unsigned where) {
-  const int n = nrow * n_sel;
+  const int n = nrow * n_sel;  // <= 128 * 4096
+  const int* base = sel + (size_t)row0 * n_sel;
+  // e / n_sel by multiplication: exact while e * n_sel < 2^32
+  const unsigned inv = n_sel > 1 ? 0xffffffffu / (unsigned)n_sel + 1u : 0u;
+#pragma unroll 4
   for (int e = threadIdx.x; e < n; e += blockDim.x) {
-    const int i = e / n_sel;
-    const int id = __ldg(sel + (size_t)row0 * n_sel + e);
-    if (id < 0) continue;
+    const int id = __ldg(base + e);
+    const int i = n_sel > 1 ? (int)__umulhi((unsigned)e, inv) : e;
     if (id >= nblk) {  // not read through
       record_error(kBadBlockId, where, (unsigned)(row0 + i), (unsigned)id);
       continue;
     }
     // a block that starts after the row's last visible key holds nothing
-    if (causal && id * kSelBlock > row0 + i + off) continue;
-    atomicOr(&bits[(size_t)id * W + (i >> 5)], 1u << (i & 31));
+    if (id < 0 || (causal && id * kSelBlock > row0 + i + off)) continue;
+    atomicOr(&bits[id * W + (i >> 5)], 1u << (i & 31));
   }
 }
 
@@ -111,6 +116,12 @@ __global__ void __launch_bounds__(256) select_lists_kernel(const SelListArgs a) 
     at += total;
     __syncthreads();
   }
+  if (a.bits)
+    for (int e = tid; e < a.nblk2 * W; e += 256) {
+      const int j = e / W, w = e - j * W;
+      a.bits[(((size_t)bh * a.nblk2 + j) * a.ntile + tile) * W + w] =
+          j < a.nblk ? sel_bits[e] : 0u;
+    }
   if (tid == 0) a.nstep[blockIdx.x] = (at + 1) / 2;
   if ((at & 1) && tid < W) words[(size_t)at * W + tid] = 0u;
   if ((at & 1) && tid == 0)  // the last step's second block: one that the
@@ -625,13 +636,16 @@ inline SelWorkspace sel_workspace(int B, int Hq, int Hkv, int Lq, int Lkv) {
 
 inline cudaError_t launch_select_lists(SelListArgs* a, const int* sel,
                                        int* nstep, unsigned* list,
-                                       unsigned* words, const SelGeom& gm,
+                                       unsigned* words, unsigned* bits,
+                                       const SelGeom& gm,
                                        int BH, int Lq, int Lkv, int n_sel,
                                        int causal, cudaStream_t st) {
   a->sel = sel;
   a->nstep = nstep;
   a->list = list;
   a->words = words;
+  a->bits = bits;
+  a->nblk2 = (gm.nblk + 1) & ~1;
   a->Lq = Lq;
   a->Lkv = Lkv;
   a->n_sel = n_sel;
@@ -664,8 +678,8 @@ cudaError_t launch_select_prefill(const SelProblem& pr, cudaStream_t st) {
   cudaError_t e = launch_select_lists(
       &a, pr.sel, reinterpret_cast<int*>(ws),
       reinterpret_cast<unsigned*>(ws + w.list),
-      reinterpret_cast<unsigned*>(ws + w.words), gm, pr.B * pr.Hkv, pr.Lq,
-      pr.Lkv, pr.n_sel, pr.causal, st);
+      reinterpret_cast<unsigned*>(ws + w.words), nullptr, gm, pr.B * pr.Hkv,
+      pr.Lq, pr.Lkv, pr.n_sel, pr.causal, st);
   if (e != cudaSuccess) return e;
 
   SelPrefillParams p;

@@ -20,9 +20,8 @@
 //
 // Before them:
 //   select_prep_kernel   -D and -lse * log2 e per query row
-//   select_lists_kernel  per tile: its blocks and their token bits
-//   select_bits_kernel   per (KV head, tile): the token bits of every block,
-//                        stored block-major
+//   select_lists_kernel  per tile: its blocks and their token bits, and the
+//                        bits of every block, block-major
 //   select_tiles_kernel  per (KV head, 128-key block): the tiles with a bit,
 //                        ascending, and their bits
 //   select_order_kernel  the key blocks by the length of their lists
@@ -34,33 +33,12 @@
 namespace blasst {
 
 struct SelBwdListArgs {
-  const int* sel;    // [B, Hkv, Lq, n_sel]
-  unsigned* bits;    // [B*Hkv][nblk2][ntile][wpt]
+  const unsigned* bits;  // [B*Hkv][nblk2][ntile][wpt]
   int* count;        // [slots], slot = jb * (B*Hkv) + b*Hkv + hkv
   int* list;         // [slots][ntile]
   unsigned* words;   // [slots][ntile][2][wpt]
-  int BH, Lq, Lkv, n_sel, causal;
-  int TQ, wpt, ntile, nblk, nblk2;  // nblk2: nblk rounded up to whole 128 keys
+  int BH, wpt, ntile, nblk2;
 };
-
-__global__ void __launch_bounds__(256)
-    select_bits_kernel(const SelBwdListArgs a) {
-  extern __shared__ unsigned sel_bits[];  // [nblk][wpt]
-  const int bh = blockIdx.x / a.ntile;
-  const int tile = blockIdx.x - bh * a.ntile;
-  for (int e = threadIdx.x; e < a.nblk * a.wpt; e += 256) sel_bits[e] = 0u;
-  __syncthreads();
-  const int row0 = tile * a.TQ;
-  sel_set_bits(a.sel + (size_t)bh * a.Lq * a.n_sel, sel_bits, a.wpt, row0,
-               min(a.TQ, a.Lq - row0), a.n_sel, a.Lkv - a.Lq, a.causal, a.nblk,
-               (unsigned)bh);
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.nblk2 * a.wpt; e += 256) {
-    const int j = e / a.wpt, w = e - j * a.wpt;
-    a.bits[(((size_t)bh * a.nblk2 + j) * a.ntile + tile) * a.wpt + w] =
-        j < a.nblk ? sel_bits[e] : 0u;
-  }
-}
 
 __global__ void __launch_bounds__(128)
     select_tiles_kernel(const SelBwdListArgs a) {
@@ -195,6 +173,7 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+constexpr int kSelNumSm = 148;  // one CTA of either pass per SM
 constexpr int kSelBwdThreads = 64 + 256;  // producer, issuer, 8 compute warps
 
 // ---------------------------------------------------------------------------
@@ -1018,40 +997,35 @@ inline cudaError_t launch_select_backward(const SelBwdProblem& pr,
                          : gm.TQ == 8 ? 0x01010101u : 0x11111111u;
   p.scale = pr.scale;
 
+  SelListArgs la;
+  cudaError_t e = launch_select_lists(
+      &la, pr.sel, reinterpret_cast<int*>(ws + w.nstep),
+      reinterpret_cast<unsigned*>(ws + w.list),
+      reinterpret_cast<unsigned*>(ws + w.words),
+      reinterpret_cast<unsigned*>(ws + w.bits), gm, BH, pr.Lq, pr.Lkv, pr.n_sel,
+      pr.causal, st);
+  if (e != cudaSuccess) return e;
+  p.nstep = la.nstep;
+  p.list = la.list;
+  p.words = la.words;
   SelBwdListArgs a;
-  a.sel = pr.sel;
-  a.bits = reinterpret_cast<unsigned*>(ws + w.bits);
+  a.bits = la.bits;
   a.count = reinterpret_cast<int*>(ws + w.count);
   a.list = reinterpret_cast<int*>(ws + w.tlist);
   a.words = reinterpret_cast<unsigned*>(ws + w.twords);
   a.BH = BH;
-  a.Lq = pr.Lq;
-  a.Lkv = pr.Lkv;
-  a.n_sel = pr.n_sel;
-  a.causal = pr.causal;
-  a.TQ = gm.TQ;
   a.wpt = gm.wpt;
   a.ntile = gm.ntile;
-  a.nblk = gm.nblk;
-  a.nblk2 = 2 * nk;
+  a.nblk2 = la.nblk2;
   p.count = a.count;
   p.tlist = a.list;
   p.twords = a.words;
-
-  select_prep_kernel<<<(unsigned)prep_blocks, 256, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  const int smem = gm.nblk * gm.wpt * 4;
-  e = cudaFuncSetAttribute(select_bits_kernel,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  select_bits_kernel<<<(unsigned)tiles, 256, smem, st>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   select_tiles_kernel<<<(unsigned)slots, 128, 0, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (slots <= kBwdOrderMaxSlots) {  // (the rank is quadratic)
+  // the order of the key blocks; none when every one has an SM to itself, or
+  // when they are so many that the quadratic rank would cost more
+  if (slots > kSelNumSm && slots <= kBwdOrderMaxSlots) {
     int* order = reinterpret_cast<int*>(ws + w.order);
     select_order_kernel<<<(unsigned)((slots + 7) / 8), 256, 0, st>>>(
         a.count, (int)slots, order);
@@ -1059,6 +1033,10 @@ inline cudaError_t launch_select_backward(const SelBwdProblem& pr,
     if (e != cudaSuccess) return e;
     p.order = order;
   }
+
+  select_prep_kernel<<<(unsigned)prep_blocks, 256, 0, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(select_dkdv_kernel,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            SelDkdvCfg::SMEM_ALLOC);
@@ -1068,15 +1046,6 @@ inline cudaError_t launch_select_backward(const SelBwdProblem& pr,
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
-  SelListArgs la;
-  e = launch_select_lists(&la, pr.sel, reinterpret_cast<int*>(ws + w.nstep),
-                          reinterpret_cast<unsigned*>(ws + w.list),
-                          reinterpret_cast<unsigned*>(ws + w.words), gm, BH,
-                          pr.Lq, pr.Lkv, pr.n_sel, pr.causal, st);
-  if (e != cudaSuccess) return e;
-  p.nstep = la.nstep;
-  p.list = la.list;
-  p.words = la.words;
   e = cudaFuncSetAttribute(select_dq_kernel,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            SelDqCfg::SMEM_ALLOC);

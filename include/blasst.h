@@ -632,8 +632,9 @@ blasst_status_t blasst_select_prefill(const void *q, const void *k,
  *             aligned, caller-owned
  * Each gradient is summed in float32 in a fixed order.  P and dS are rounded
  * to bf16 for their tensor-core products, and D = dO . O uses the bf16 o.
- * Asynchronous on `stream`; seven kernel launches (six when B * Hkv *
- * ceil(Lkv/128) exceeds 32768); allocates nothing.
+ * Asynchronous on `stream`; six kernel launches (five when the key blocks,
+ * B * Hkv * ceil(Lkv/128), are at most 148 or more than 32768); allocates
+ * nothing.
  */
 size_t blasst_select_prefill_backward_workspace_size(int B, int Hq, int Hkv,
                                                      int Lq, int Lkv, int d);
