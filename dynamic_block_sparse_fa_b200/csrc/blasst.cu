@@ -1461,13 +1461,15 @@ int blasst_select_decode_splits(int B, int Hq, int Hkv, int n_sel) {
   const int G = Hq / Hkv;
   const long long units = (long long)B * Hkv * (G > 8 ? G / 8 : 1);
   // the waves of 3 CTAs per SM times one item's blocks and its fixed cost
-  // (the list, q, its partial and merge row: about 3 blocks' time)
+  // (the list, q, its partial and merge row: about 6 blocks' time; batch 32
+  // x 8 KV heads with 64 blocks: 3 splits, 96 us, against 99 for 5, 107 for 1
+  // and 110 for 4)
   const long long slots = (long long)kNumSmB200 * 3;
   long long best = 1;
   double best_t = 0.0;
   for (long long s = 1; s <= n_sel; ++s) {
     const double waves = std::ceil((double)(units * s) / (double)slots);
-    const double t = waves * (std::ceil((double)n_sel / (double)s) + 3.0);
+    const double t = waves * (std::ceil((double)n_sel / (double)s) + 6.0);
     if (s == 1 || t < best_t - 1e-9) {
       best_t = t;
       best = s;

@@ -181,11 +181,16 @@ __device__ __forceinline__ int sel_compact(const int* sel, int n_sel, int nk,
     raw[e] = id;
   }
   if (__syncthreads_or(bad)) return -1;
+  // an ascending list (block_select's) repeats nothing
+  bool loose = false;
+  for (int e = tid; e < n_sel; e += kDecThreads)
+    loose |= e > 0 && raw[e] >= 0 && (raw[e - 1] < 0 || raw[e] <= raw[e - 1]);
+  const bool search = __syncthreads_or(loose);
   int at = 0;
   for (int e0 = 0; e0 < n_sel; e0 += kDecThreads) {
     const int e = e0 + tid;
     bool take = e < n_sel && raw[e] >= 0;
-    if (take) {
+    if (take && search) {
       const int id = raw[e];
       for (int x = 0; x < e; ++x)
         if (raw[x] == id) {
