@@ -295,30 +295,61 @@ struct RowTask {
   float eps;
 };
 
-// The same cut for one warp whose n <= 32 NR finite scores fit its registers:
+// A row's scores for one warp, lane l holding every 32nd from l: in NR
+// registers, or (NR 0) where they are.  each(f) calls f(x, score 32 x + lane),
+// -infinity past the end.
+template <int NR>
+struct RowScores {
+  float v[NR];
+  __device__ __forceinline__ explicit RowScores(const RowTask& r) {
+#pragma unroll
+    for (int x = 0; x < NR; ++x) {
+      const int i = 32 * x + (int)(threadIdx.x & 31);
+      v[x] = i < r.n ? r.s[i] : -INFINITY;
+    }
+  }
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+#pragma unroll
+    for (int x = 0; x < NR; ++x) f(x, v[x]);
+  }
+};
+template <>
+struct RowScores<0> {
+  const float* s;
+  int n;
+  __device__ __forceinline__ explicit RowScores(const RowTask& r)
+      : s(r.s), n(r.n) {}
+  template <class F>
+  __device__ __forceinline__ void each(F f) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 4
+    for (int x = 0; x < (n + 31) / 32; ++x)
+      f(x, 32 * x + lane < n ? s[32 * x + lane] : -INFINITY);
+  }
+};
+
+// The same cut by one warp for n finite scores:
 // t splits off exactly k (split), or equal values at t (or a float step above
 // it) straddle the cut.  A prompt has a row per token and KV head, so this
 // sets the selection's time.  The first thresholds come from the normal
 // distribution of the scores' mean and variance (a score sums d products) and
 // from its density there, the next from bisection: about 4 passes of NR
 // compares and one warp reduction where bisection alone takes 9.
-template <int NR>
-__device__ __forceinline__ void find_cut(const RowTask& r, float (&v)[NR],
+template <class ScoresT>
+__device__ __forceinline__ void find_cut(const RowTask& r, const ScoresT& v,
                                          float& t, bool& split) {
   const int lane = threadIdx.x & 31;
   // at least k values are >= lo; fewer than k are >= hi, or hi is the maximum
   float lo = INFINITY, hi = -INFINITY, s1 = 0.f, s2 = 0.f;
-#pragma unroll
-  for (int x = 0; x < NR; ++x) {
-    const int i = 32 * x + lane;
-    const bool in = i < r.n;
-    v[x] = in ? r.s[i] : -INFINITY;
-    hi = fmaxf(hi, v[x]);
-    lo = fminf(lo, in ? v[x] : INFINITY);
-    const float z = in ? v[x] : 0.f;
+  v.each([&](int x, float z) {
+    const bool in = 32 * x + lane < r.n;
+    hi = fmaxf(hi, z);
+    lo = fminf(lo, in ? z : INFINITY);
+    z = in ? z : 0.f;
     s1 += z;
     s2 = fmaf(z, z, s2);
-  }
+  });
   hi = redux_max(hi);
   lo = redux_min(lo);
 #pragma unroll
@@ -341,8 +372,7 @@ __device__ __forceinline__ void find_cut(const RowTask& r, float (&v)[NR],
   if (!(t > lo && t < hi)) t = lo;  // one value, or no float between two
   for (int pass = 0; t > lo; ++pass) {
     int c = 0;
-#pragma unroll
-    for (int x = 0; x < NR; ++x) c += v[x] >= t;
+    v.each([&](int, float y) { c += y >= t; });
     const int d = (int)__reduce_add_sync(~0u, (unsigned)c) - r.k;
     if (d == 0) {
       split = true;
@@ -362,30 +392,28 @@ __device__ __forceinline__ void find_cut(const RowTask& r, float (&v)[NR],
 // the equal values lie within a float step of t, far inside 2 eps.)  Returns
 // false, with nothing written, when they are more than 32, or when equal
 // scores straddle the cut and eps is 0.
-template <int NR, class ExactT>
-__device__ __forceinline__ bool take_cut(const RowTask& r, const float (&v)[NR],
+template <class ScoresT, class ExactT>
+__device__ __forceinline__ bool take_cut(const RowTask& r, const ScoresT& v,
                                          float t, bool split, ExactT exact) {
   const int lane = threadIdx.x & 31;
+  const unsigned below = (1u << lane) - 1u;
   int* out = r.out;
   float a = t, b = t;  // smallest taken, largest left
   if (split) {
     a = INFINITY;
     b = -INFINITY;
-#pragma unroll
-    for (int x = 0; x < NR; ++x) {
-      if (v[x] >= t) a = fminf(a, v[x]);
-      else b = fmaxf(b, v[x]);
-    }
+    v.each([&](int, float y) {
+      if (y >= t) a = fminf(a, y);
+      else b = fmaxf(b, y);
+    });
     a = redux_min(a);
     b = redux_max(b);
     if (a - b > 2.f * r.eps) {
-#pragma unroll
-      for (int x = 0; x < NR; ++x) {
-        const bool take = v[x] >= t;
-        const unsigned m = __ballot_sync(~0u, take);
-        if (take) out[__popc(m & ((1u << lane) - 1u))] = r.f + 32 * x + lane;
+      v.each([&](int x, float y) {
+        const unsigned m = __ballot_sync(~0u, y >= t);
+        if (y >= t) out[__popc(m & below)] = r.f + 32 * x + lane;
         out += __popc(m);
-      }
+      });
       return true;
     }
   } else if (r.eps == 0.f) {
@@ -394,57 +422,50 @@ __device__ __forceinline__ bool take_cut(const RowTask& r, const float (&v)[NR],
   const float up = b + 2.f * r.eps;  // above: taken for certain
   const float dn = a - 2.f * r.eps;  // below: left for certain
   int sure = 0, cnt = 0;
-#pragma unroll
-  for (int x = 0; x < NR; ++x) {
-    sure += __popc(__ballot_sync(~0u, v[x] > up));
-    cnt += __popc(__ballot_sync(~0u, v[x] >= dn && v[x] <= up));
-  }
+  v.each([&](int, float y) {
+    sure += __popc(__ballot_sync(~0u, y > up));
+    cnt += __popc(__ballot_sync(~0u, y >= dn && y <= up));
+  });
   if (cnt > 32) return false;
+  // lane o gets the o-th doubtful block, in ascending order
+  int mine_at = 0, at = 0;
+  v.each([&](int x, float y) {
+    unsigned m = __ballot_sync(~0u, y >= dn && y <= up);
+    for (; m; m &= m - 1, ++at)
+      if (lane == at) mine_at = 32 * x + __ffs(m) - 1;
+  });
   double mine = 0.0;
-  int at = 0;
-#pragma unroll 1
-  for (int x = 0; x < NR; ++x) {
-    float vx = v[0];
-#pragma unroll
-    for (int y = 1; y < NR; ++y) vx = x == y ? v[y] : vx;
-    unsigned m = __ballot_sync(~0u, vx >= dn && vx <= up);
-    while (m) {
-      const int l = __ffs(m) - 1;
-      m &= m - 1;
-      const double e = exact(r.f + 32 * x + l);
-      if (lane == at) mine = e;
-      ++at;
-    }
+  for (int o = 0; o < cnt; ++o) {
+    const double e = exact(r.f + __shfl_sync(~0u, mine_at, o));
+    if (lane == o) mine = e;
   }
   int ahead = 0;  // doubtful blocks that go before this lane's
   for (int o = 0; o < cnt; ++o) {
     const double e = __shfl_sync(~0u, mine, o);
     ahead += e > mine || (e == mine && o < lane);
   }
-  // of the doubtful blocks, in ascending order
   unsigned won = __ballot_sync(~0u, lane < cnt && ahead < r.k - sure);
-#pragma unroll
-  for (int x = 0; x < NR; ++x) {
-    const bool doubt = v[x] >= dn && v[x] <= up;
+  v.each([&](int x, float y) {
+    const bool doubt = y >= dn && y <= up;
     unsigned m = __ballot_sync(~0u, doubt);
-    const bool take =
-        v[x] > up || (doubt && ((won >> __popc(m & ((1u << lane) - 1u))) & 1u));
+    const bool take = y > up || (doubt && ((won >> __popc(m & below)) & 1u));
     const int c = __popc(m);
     won = c < 32 ? won >> c : 0u;
     m = __ballot_sync(~0u, take);
-    if (take) out[__popc(m & ((1u << lane) - 1u))] = r.f + 32 * x + lane;
+    if (take) out[__popc(m & below)] = r.f + 32 * x + lane;
     out += __popc(m);
-  }
+  });
   return true;
 }
 
-// Cut and take of one row whose n <= 32 NR; false: left to take_general.
+// Cut and take of one row (n <= 32 NR, or NR 0); false: left to take_general.
 template <int NR, class ExactT>
 __device__ __forceinline__ bool take_row(const RowTask& r, ExactT exact) {
-  float v[NR], t;
+  const RowScores<NR> v(r);
+  float t;
   bool split;
-  find_cut<NR>(r, v, t, split);
-  return take_cut<NR>(r, v, t, split, exact);
+  find_cut(r, v, t, split);
+  return take_cut(r, v, t, split, exact);
 }
 
 // The take of one row in general, by a warp or a CTA, for any n: s is
@@ -715,9 +736,10 @@ __global__ void __launch_bounds__(kSelDecThreads, 2)
     }
     return exact_score<D>(qd, c0 + (size_t)j * D);
   };
-  // One warp's registers hold the scores of up to 1024 blocks (65536
-  // tokens): its reductions cost an instruction where the CTA's cost a
-  // barrier.  The other warps are done.
+  // Up to 1024 blocks (65536 tokens) one warp selects: its reductions cost an
+  // instruction where the CTA's cost a barrier (batch 32 x 8 KV heads at 64K:
+  // 31 us against 33; at 128K one warp takes 54 us, the CTA 47).  The other
+  // warps are done.
   __shared__ int by_cta;
   if (warp == 0) {
     WarpGroup wg;
@@ -725,7 +747,7 @@ __global__ void __launch_bounds__(kSelDecThreads, 2)
     if (todo && eps < INFINITY) {
       if (n <= 256) todo = !take_row<8>(task, exact);
       else if (n <= 512) todo = !take_row<16>(task, exact);
-      else if (n <= 1024) todo = !take_row<32>(task, exact);
+      else if (n <= 1024) todo = !take_row<0>(task, exact);
     }
     if (lane == 0) by_cta = todo;
   }
@@ -990,6 +1012,7 @@ __global__ void __launch_bounds__(256, 3)
       else if (task.n <= 128) todo = !take_row<4>(task, exact);
       else if (task.n <= 256) todo = !take_row<8>(task, exact);
       else if (task.n <= 512) todo = !take_row<16>(task, exact);
+      else todo = !take_row<0>(task, exact);
     }
     if (todo) take_general(g, srow, task, exact);
     __syncwarp();

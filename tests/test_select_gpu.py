@@ -854,3 +854,46 @@ def test_select_scores_as_large_as_their_bound(m):
     got = m.blasst_block_select(q, c, 19200, n_sel=40, causal=False)
     _clean(m)
     assert torch.equal(got.cpu(), _ref_select(q, c, 19200, False, 40, 1, 1))
+
+
+@pytest.mark.parametrize("nb", [600, 2048])
+def test_select_near_ties_of_long_rows(m, nb):
+    """Rows of more blocks than a warp's registers hold."""
+    g = _gen(nb)
+    base = _rand(g, 128).float()
+    c = base.repeat(1, 1, nb, 1)
+    at = torch.randint(0, 128, (nb,), generator=g, device="cuda")
+    c[0, 0, torch.arange(nb, device="cuda"), at] *= 1 + 2.0 ** -7
+    c = c.to(BF)
+    c[0, 0, 300:330] = _rand(g, 30, 128)
+    c[0, 0, 500:520] = c[0, 0, 480:500]
+    q = _rand(g, 1, 4, 24, 128)
+    q[:, :, 3] = 0
+    for n in (9, 45):
+        got = m.blasst_block_select(q, c, nb * 64, n_sel=n, causal=False)
+        _clean(m)
+        assert torch.equal(got.cpu(),
+                           _ref_select(q, c, nb * 64, False, n, 1, 1))
+
+
+@pytest.mark.parametrize("G", [1, 4])
+def test_longest_prompt_keys(m, G):
+    """262144 keys: the whole range of block ids, lists as long as n_sel
+    allows, forward and backward."""
+    Lq, Lkv = 5, 262144
+    g = _gen(90 + G)
+    q, k, v = _qkv(g, 1, G, 1, Lq, Lkv, 128)
+    do = _rand(g, 1, G, Lq, 128)
+    sel = torch.full((1, 1, Lq, 4096), -1, dtype=torch.int32, device="cuda")
+    sel[0, 0, 0, :3] = torch.tensor([0, 4095, 2047], device="cuda").int()
+    sel[0, 0, 1] = torch.randint(0, 4096, (4096,), generator=g,
+                                 device="cuda").int()
+    sel[0, 0, 2, 4000:] = 17
+    sel[0, 0, 4, ::2] = torch.arange(4095, 2047, -1, device="cuda").int()
+    o, lse = m.blasst_select_prefill(q, k, v, sel, scale=0.05)
+    got = m.blasst_select_prefill_backward(q, k, v, o, lse, do, sel, scale=0.05)
+    _clean(m)
+    ref = R.attention(q, k, v, sel, 0.05, True, do)
+    _check_o(o, ref, lse, G)
+    for name, t in zip(("dq", "dk", "dv"), got):
+        _check_grad(t, ref[name], name)
