@@ -197,9 +197,14 @@ struct SelPrefillCfg {
 // long as its exps alone keep the MUFU busy, so two groups of 4 warps (thread
 // = row) take the even and the odd steps and overlap: while one group is in
 // its exps the other loads, reduces and stores.  All they share is the row's
-// running max and reference, handed over once per step before the exps.  S of
-// step s + 2 is issued as soon as step s has read its scores, so the chain
-// never waits for the tensor core.
+// running max and reference, handed over once per step after three quarters of
+// its exps, so that the groups' exps follow one another.  S of step s + 2 is
+// issued as soon as step s has read its scores, so the chain never waits for
+// the tensor core.
+//
+// 32 heads on 8, 16K causal, 32 blocks a row: 0.82 ms, the tensor pipe and the
+// MUFU 48% busy each (1024 cycles of either a step, of about 1.9k); 0.9 PFLOP/s
+// of 128 x 128 tiles, 0.62 of the rows' own blocks.
 template <int D>
 __global__ void __launch_bounds__(352, 1)
     select_prefill_kernel(const __grid_constant__ SelPrefillParams p) {
