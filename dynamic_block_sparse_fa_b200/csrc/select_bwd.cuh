@@ -12,8 +12,8 @@
 //                       blocks its tokens selected, two a step
 // That is 4 + 3 products of 128^3 a pair where one pass over the pairs needs
 // 5, but the one pass has to add every pair's dQ tile (64 KB of float32) to
-// memory: at train_8k's sizes (8K causal, 32 heads on 8, 16 blocks a row) the
-// additions alone cost 370 of its 1190 us, they leave the tensor memory no
+// memory: at 8K causal, 32 heads on 8, 16 blocks a row, the additions alone
+// cost 370 of its 1190 us, they leave the tensor memory no
 // room to overlap the products with the threads' work, and their order
 // changes the result from run to run.  The dQ pass also walks 64-key blocks,
 // a third fewer than the 128-key pairs.  Both passes sum in a fixed order.
