@@ -188,6 +188,11 @@ constexpr int kSelBwdThreads = 64 + 256;  // producer, issuer, 8 compute warps
 // (38.6k pairs): 0.52 ms, the tensor pipe 60% busy; what bounds a pair is the
 // hand-offs between its products and the threads' two phases.
 // ---------------------------------------------------------------------------
+template <bool V>
+struct BoolTag {
+  static constexpr bool value = V;
+};
+
 struct SelDkdvCfg {
   static constexpr int TILE = 128 * kBwdD * 2;  // 32 KB, two 64-column boxes
   static constexpr int BOX = 128 * 128;
@@ -391,6 +396,26 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
                                         (size_t)p.wpt;
     const int w0 = (2 * wg) & (p.wpt - 1), w1 = (2 * wg + 1) & (p.wpt - 1);
     bool ok = true;
+    // A V row with an infinity or NaN makes its dP so everywhere: where one of
+    // the warp's rows has any, dS of hidden entries is set to 0 (a key that
+    // nobody selected has no gradient, whatever it holds).
+    bool odd_v = false;
+    if (nt > 0) {
+      const bool w = mbar_wait(&bar[C::B_KV], 0, kWaitSelect, 0, 519);
+      ok = __all_sync(FULL, w);
+      bool odd = false;
+#pragma unroll 4
+      for (int e = 0; e < 16; ++e) {
+        const uint4 x = *reinterpret_cast<const uint4*>(
+            smem + C::OFF_V + (e >> 3) * C::BOX + rr * 128 + (e & 7) * 16);
+        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          odd |= (y[i] & 0x7f800000u) == 0x7f800000u ||
+                 (y[i] & 0x7f80u) == 0x7f80u;
+      }
+      odd_v = __any_sync(FULL, odd);
+    }
     // P of a tile from its P phase to its dS phase, as fp16: 2^-11 of it, so
     // that the bf16 rounding of dS is the only one that counts (below 6e-5
     // fp16 is subnormal: off by at most 3e-8, of weights that sum to 1)
@@ -486,26 +511,37 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
       ok = __all_sync(FULL, w);
       if (!ok) break;
       tc_fence_after();
+      auto d_phase = [&](auto hide) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint32_t dp[32], st[16];
-        tmem_ld32(lane_base + 128 + u * 32, dp);
-        tc_wait_ld();
+        for (int u = 0; u < 2; ++u) {
+          uint32_t dp[32], st[16];
+          tmem_ld32(lane_base + 128 + u * 32, dp);
+          tc_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 32; x += 4) {
-          const float4 d4 = del4[u * 8 + (x >> 2)];
-          const float2 pa = unpack_f16x2(pk[u * 16 + (x >> 1)]);
-          const float2 pb = unpack_f16x2(pk[u * 16 + (x >> 1) + 1]);
-          float s0, s1, s2, s3;
-          add_mul2(s0, s1, pa.x, pa.y, __uint_as_float(dp[x]),
-                   __uint_as_float(dp[x + 1]), d4.x, d4.y);
-          add_mul2(s2, s3, pb.x, pb.y, __uint_as_float(dp[x + 2]),
-                   __uint_as_float(dp[x + 3]), d4.z, d4.w);
-          st[x >> 1] = pack_bf16x2(s0, s1);
-          st[(x >> 1) + 1] = pack_bf16x2(s2, s3);
+          for (int x = 0; x < 32; x += 4) {
+            const float4 d4 = del4[u * 8 + (x >> 2)];
+            const float2 pa = unpack_f16x2(pk[u * 16 + (x >> 1)]);
+            const float2 pb = unpack_f16x2(pk[u * 16 + (x >> 1) + 1]);
+            float ds[4];
+            add_mul2(ds[0], ds[1], pa.x, pa.y, __uint_as_float(dp[x]),
+                     __uint_as_float(dp[x + 1]), d4.x, d4.y);
+            add_mul2(ds[2], ds[3], pb.x, pb.y, __uint_as_float(dp[x + 2]),
+                     __uint_as_float(dp[x + 3]), d4.z, d4.w);
+            if constexpr (decltype(hide)::value) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                ds[e] = (cm[u] >> (x + e)) & 1u ? ds[e] : 0.f;
+            }
+            st[x >> 1] = pack_bf16x2(ds[0], ds[1]);
+            st[(x >> 1) + 1] = pack_bf16x2(ds[2], ds[3]);
+          }
+          tmem_st16(lane_base + 128 + u * 16, st);
         }
-        tmem_st16(lane_base + 128 + u * 16, st);
-      }
+      };
+      if (odd_v)  // warp-uniform
+        d_phase(BoolTag<true>());
+      else
+        d_phase(BoolTag<false>());
       tc_wait_st();
       tc_fence_before();
       __syncwarp();

@@ -520,9 +520,11 @@ int blasst_mla_decode_splits(int B, int L);
  * selected no visible key gives o = 0, lse = -inf and no gradient.
  *
  * Non-finite values: K and V rows of blocks that no query of a tile selected
- * are not read.  The rows of a tile (128 Hkv/Hq neighbouring tokens of the
- * heads of a KV head) share their blocks' V, so an infinity or NaN in a V row
- * reaches every query of a tile that selected its block, masked or not.
+ * change nothing (their gradients are 0).  The rows of a tile (128 Hkv/Hq
+ * neighbouring tokens of the heads of a KV head) share the blocks any of them
+ * selected: a V row that is infinite or NaN (in the backward a K row too, and
+ * for dK and dV a q or dout row) reaches every row of such a tile, masked or
+ * not.  A K row the forward masks may hold anything.
  */
 #define BLASST_SELECT_BLOCK 64
 

@@ -897,3 +897,26 @@ def test_longest_prompt_keys(m, G):
     _check_o(o, ref, lse, G)
     for name, t in zip(("dq", "dk", "dv"), got):
         _check_grad(t, ref[name], name)
+
+
+def test_backward_unselected_blocks_may_hold_anything(m):
+    """Infinities and NaN in K and V of blocks nobody selected, next to selected
+    ones inside the same 128 keys: gradients of the others as without them,
+    their own 0."""
+    q, k, v = _qkv(_gen(95), 1, 4, 1, 256, 640, 128)
+    do = _rand(_gen(96), 1, 4, 256, 128)
+    sel = torch.tensor([1, 4, 9], dtype=torch.int32,
+                       device="cuda").expand(1, 1, 256, 3).contiguous()
+    sel[0, 0, 40:50] = -1
+    ref = R.attention(q, k, v, sel, 0.1, False, do)
+    for j in (0, 2, 3, 5, 6, 7, 8):
+        k[:, :, j * 64:(j + 1) * 64] = math.nan
+        v[:, :, j * 64:(j + 1) * 64] = math.inf
+    dq, dk, dv = _train(m, q, k, v, sel, do, 0.1, False)
+    _clean(m)
+    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+        _check_grad(t, ref[name], name)
+    hid = torch.ones(640, dtype=torch.bool, device="cuda")
+    for j in (1, 4, 9):
+        hid[j * 64:(j + 1) * 64] = False
+    assert (dk[0, 0, hid] == 0).all() and (dv[0, 0, hid] == 0).all()
