@@ -5,7 +5,6 @@
 
 #include <cstdint>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 namespace blasst {
@@ -386,14 +385,6 @@ __device__ __forceinline__ float bf16hi(uint32_t w) {
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 unpack_f16x2(uint32_t w) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
 // ---------------------------------------------------------------------------

@@ -416,10 +416,12 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
       }
       odd_v = __any_sync(FULL, odd);
     }
-    // P of a tile from its P phase to its dS phase, as fp16: 2^-11 of it, so
-    // that the bf16 rounding of dS is the only one that counts (below 6e-5
-    // fp16 is subnormal: off by at most 3e-8, of weights that sum to 1)
-    uint32_t pk[32];
+    // P of a tile from its P phase to its dS phase, float32: a weight far below
+    // its row's largest still gives its key a gradient, and the bf16 rounding
+    // of dS is the only one that counts.  (Half the registers would hold it as
+    // bf16 or fp16: fp16 loses the weights below 3e-8, bf16 adds an error as
+    // large as that rounding.)
+    float pf[64];
     unsigned m_n[2] = {0u, 0u};  // next tile's token bits
     int t_n = 0;                 // and the tile
     if (nt > 0) {
@@ -479,14 +481,16 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
             p3 = ex2_approx(p3);
             st[x >> 1] = pack_bf16x2(p0, p1);
             st[(x >> 1) + 1] = pack_bf16x2(p2, p3);
-            pk[u * 16 + (x >> 1)] = pack_f16x2(p0, p1);
-            pk[u * 16 + (x >> 1) + 1] = pack_f16x2(p2, p3);
+            pf[u * 32 + x] = p0;
+            pf[u * 32 + x + 1] = p1;
+            pf[u * 32 + x + 2] = p2;
+            pf[u * 32 + x + 3] = p3;
           }
         } else {
 #pragma unroll
           for (int x = 0; x < 32; x += 4) {
             const float4 l4 = lse4[u * 8 + (x >> 2)];
-            float pv[4];
+            float* pv = pf + u * 32 + x;
             fma2v(pv[0], pv[1], __uint_as_float(sv[x]), __uint_as_float(sv[x + 1]),
                   sl2, l4.x, l4.y);
             fma2v(pv[2], pv[3], __uint_as_float(sv[x + 2]),
@@ -496,8 +500,6 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
               pv[e] = (cm[u] >> (x + e)) & 1u ? ex2_approx(pv[e]) : 0.f;
             st[x >> 1] = pack_bf16x2(pv[0], pv[1]);
             st[(x >> 1) + 1] = pack_bf16x2(pv[2], pv[3]);
-            pk[u * 16 + (x >> 1)] = pack_f16x2(pv[0], pv[1]);
-            pk[u * 16 + (x >> 1) + 1] = pack_f16x2(pv[2], pv[3]);
           }
         }
         tmem_st16(lane_base + u * 16, st);
@@ -520,12 +522,11 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
 #pragma unroll
           for (int x = 0; x < 32; x += 4) {
             const float4 d4 = del4[u * 8 + (x >> 2)];
-            const float2 pa = unpack_f16x2(pk[u * 16 + (x >> 1)]);
-            const float2 pb = unpack_f16x2(pk[u * 16 + (x >> 1) + 1]);
+            const float* pv = pf + u * 32 + x;
             float ds[4];
-            add_mul2(ds[0], ds[1], pa.x, pa.y, __uint_as_float(dp[x]),
+            add_mul2(ds[0], ds[1], pv[0], pv[1], __uint_as_float(dp[x]),
                      __uint_as_float(dp[x + 1]), d4.x, d4.y);
-            add_mul2(ds[2], ds[3], pb.x, pb.y, __uint_as_float(dp[x + 2]),
+            add_mul2(ds[2], ds[3], pv[2], pv[3], __uint_as_float(dp[x + 2]),
                      __uint_as_float(dp[x + 3]), d4.z, d4.w);
             if constexpr (decltype(hide)::value) {
 #pragma unroll
