@@ -472,6 +472,12 @@ __device__ __forceinline__ bool take_row(const RowTask& r, ExactT exact) {
 // The take of one row in general, by a warp or a CTA, for any n: s is
 // overwritten where the cut needs it.  exact(j) (taken by a whole warp) is the
 // float64 score of block j.
+//
+// Blocks whose place a cut leaves open are scored again, as the distance of
+// their exact score to a reference among them, rounded to float32.  Rounding
+// keeps the order, so after another cut only blocks that tie there are open;
+// the next round takes the first of them as its reference, and the rounds end
+// when the tied blocks equal it in float64.
 template <class GroupT, class ExactT>
 __device__ void take_general(GroupT& g, float* s, const RowTask& r,
                              ExactT exact) {
@@ -480,37 +486,54 @@ __device__ void take_general(GroupT& g, float* s, const RowTask& r,
   const int lane = threadIdx.x & 31;
   int* out = r.out;
   Cut c;
-  bool again = !(eps < INFINITY);  // a bound that overflowed: all exact
-  if (again) {
-    c = {0.f, -INFINITY, INFINITY};
-  } else {
+  float lo = -INFINITY, hi = INFINITY;  // open: lo <= s <= hi
+  double ref = 0.0;
+  bool again = !(eps < INFINITY);  // a bound that overflowed: all are open
+  if (!again) {
     c = find_cut(g, s, n, k);
     // the scores are exact when eps is 0; otherwise the order is certain
-    // only when the cut is wider than the two errors
+    // only when the cut is wider than the two errors: above b + 2 eps is
+    // better than every value left out, below a - 2 eps worse than all taken
     again = eps > 0.f && !(c.a - c.b > 2.f * eps);
+    lo = c.a - 2.f * eps;
+    hi = c.b + 2.f * eps;
+    ref = (double)c.v;
   }
-  if (again) {
-    // above b + 2 eps: better than every value left out; below a - 2 eps:
-    // worse than all k taken; between: the distance of the exact score to
-    // the cut, whose rounding to float32 is relative to that distance
-    const float up = c.b + 2.f * eps, dn = c.a - 2.f * eps;
-    const bool all = !(eps < INFINITY);
+  bool nan_only = false;  // -infinities against NaN, which ranks below them
+  for (bool start = true; again; start = false) {
     g.sync();
     for (int i0 = 32 * g.warp; i0 < n; i0 += 32 * g.nwarps) {
       const int i = i0 + lane;
       const float x = i < n ? s[i] : 0.f;
-      float y = x > up ? INFINITY : -INFINITY;
-      unsigned todo = __ballot_sync(~0u, i < n && (all || !(x > up || x < dn)));
+      float y = x > hi ? INFINITY : -INFINITY;
+      unsigned todo = __ballot_sync(~0u, i < n && x >= lo && x <= hi);
       while (todo) {
         const int t = __ffs(todo) - 1;
         todo &= todo - 1;
-        const double e = exact(r.f + i0 + t) - (double)c.v;
-        if (lane == t) y = isnan(e) ? -INFINITY : (float)e;
+        const double e = exact(r.f + i0 + t) - ref;
+        if (lane == t) {
+          y = (float)e;
+          if (y == 0.f && e != 0.0) y = copysignf(1e-45f, y);  // 0 is 0 only
+          if (nan_only) y = 0.f;
+          if (isnan(e)) y = -INFINITY;
+        }
       }
       if (i < n) s[i] = y;
     }
     g.sync();
     c = find_cut(g, s, n, k);
+    again = c.a == c.b && c.v < INFINITY && !nan_only &&
+            (start || c.v != 0.f);
+    if (!again) break;
+    lo = hi = c.v;
+    nan_only = c.v == -INFINITY;
+    ref = 0.0;
+    if (!nan_only) {
+      float first = -INFINITY;
+      for (int i = g.id; i < n; i += GroupT::kThreads)
+        if (s[i] == c.v) first = fmaxf(first, -(float)i);
+      ref = exact(r.f - (int)g.max(first));
+    }
   }
   // values above the cut, then equal ones in ascending index
   int left = k;

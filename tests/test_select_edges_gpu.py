@@ -3,8 +3,12 @@
 Selections are whole numbers and have to be equal.  Other tolerances are
 derived where they are used.
 """
+import math
+
 import pytest
 import torch
+
+from tests import _select_ref as R
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -75,3 +79,91 @@ def test_backward_of_weakly_weighted_keys(m):
         err = (got[0, 0].double() - ref).abs()
         tol = tol * (1 + 2 ** -8) + 2 ** -8 * ref.abs()
         assert (err <= tol).all(), (name, (err / tol).max().item())
+
+
+# ------------------------------------------ scores that only 64 bits tell apart
+def _close_means(g, nb, d, f=1.0):
+    """Means whose scores against a query agree to 2^-29 of their size: one
+    vector, and in the last column 2^-30 (1 + x / 128) with x in some order."""
+    c = torch.randn(d, generator=g, device="cuda").repeat(nb, 1)
+    x = torch.randperm(nb, generator=g, device="cuda") % 128
+    c[:, d - 1] = 2.0 ** -30 * (1 + x / 128)
+    return (c.to(BF).float() * f).to(BF)
+
+
+def _close_query(g, G, R_, d, f=1.0):
+    q = torch.randn(G, R_, d, generator=g, device="cuda")
+    q[..., d - 1] = q[..., d - 1].abs() + 0.5
+    return (q.to(BF).float() * f).to(BF)
+
+
+def _check_prompt(m, q, c, causal, n, off=0, nf=1, nl=1):
+    G, Lq, _ = q.shape
+    nb = c.shape[0]
+    Lkv = Lq + off if causal else nb * 64
+    assert R.nblk(Lkv) == nb
+    got = m.blasst_block_select(q[None], c[None, None], Lkv, n_sel=n,
+                                n_first=nf, n_local=nl, causal=causal)
+    _clean(m)
+    last = [(r + off if causal else Lkv - 1) // 64 for r in range(Lq)]
+    want = R.select(q.cpu(), c.cpu(), last, n, nf, nl)
+    assert torch.equal(got[0, 0].cpu(), want)
+
+
+def _check_one(m, q, c, n):
+    nb = c.shape[0]
+    lens = torch.tensor([nb * 64], dtype=torch.int32, device="cuda")
+    got = m.blasst_block_select_decode(q[:, 0].contiguous()[None], c[None, None], lens,
+                                       n_sel=n)
+    _clean(m)
+    want = R.select(q[:, :1].cpu(), c.cpu(), [nb - 1], n, 1, 1)[0]
+    assert torch.equal(got[0, 0].cpu(), want)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("odd", [math.nan, math.inf, -math.inf])
+def test_select_close_scores_beside_a_nonfinite_mean(m, d, odd):
+    """A mean that is infinite or NaN takes its own place; the others are
+    still told apart beyond float32's resolution."""
+    g = _gen(3)
+    q = _close_query(g, 2, 40, d)
+    c = _close_means(g, 100, d)
+    c[30, 7] = odd
+    _check_prompt(m, q, c, False, 20)
+    # a block that only the last rows of a 16-row tile see, and one that no
+    # row of the tile sees
+    q2 = _close_query(g, 2, 500, d)
+    for at in (50, 51, 55):
+        c = _close_means(g, 59, d)
+        c[at, 7] = odd
+        # rows 0 .. 7 end in block 50, rows 8 .. 71 in block 51
+        _check_prompt(m, q2, c, True, 20, off=64 * 51 - 8)
+    for nb in (200, 400, 700, 1500):
+        c = _close_means(g, nb, d)
+        c[nb // 3, 7] = odd
+        _check_one(m, q, c, 30)
+
+
+def test_select_nan_below_minus_infinity(m):
+    """A NaN score ranks below every other, -infinity among them."""
+    c = torch.ones(70, 64, device="cuda", dtype=BF)
+    q = torch.ones(1, 3, 64, device="cuda", dtype=BF)
+    c[5, 0] = math.nan
+    c[9:20, 0] = -math.inf
+    want = torch.tensor([j for j in range(70) if j != 5], dtype=torch.int32)
+    got = m.blasst_block_select(q[None], c[None, None], 70 * 64, n_sel=69,
+                                causal=False)
+    assert (got[0, 0].cpu() == want).all()
+    lens = torch.tensor([70 * 64], dtype=torch.int32, device="cuda")
+    got = m.blasst_block_select_decode(q[:, 0].contiguous()[None], c[None, None], lens,
+                                       n_sel=69)
+    _clean(m)
+    assert (got[0, 0].cpu() == want).all()
+
+
+@pytest.mark.parametrize("f", [1e8, 1e17, 1e30])
+def test_select_close_scores_of_large_means(m, f):
+    g = _gen(4)
+    q = _close_query(g, 2, 20, 128)
+    _check_prompt(m, q, _close_means(g, 90, 128, f), False, 20)
+    _check_one(m, q, _close_means(g, 300, 128, f), 40)
