@@ -167,3 +167,36 @@ def test_select_close_scores_of_large_means(m, f):
     q = _close_query(g, 2, 20, 128)
     _check_prompt(m, q, _close_means(g, 90, 128, f), False, 20)
     _check_one(m, q, _close_means(g, 300, 128, f), 40)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_select_scores_the_tensor_core_cuts_most(m, d):
+    """Two blocks whose float32 scores are in the wrong order by more than
+    2^-17 |x| |c|: every product of the better one (A) but the first ends just
+    below a multiple of 2^-25 of the sum, where the tensor core cuts it off,
+    and so do those of the other (B), with the other sign."""
+    n = d // 16                  # steps; a d of 64 loses half as much
+    x = torch.full((d,), 2.0 ** -12)
+    x[0], x[1] = 1.0, 2.0 ** -8
+    under = 255 / 128            # the largest bf16 below 2
+    a = torch.full((d,), under * 2.0 ** -13)
+    a[15::16] /= 2               # 15 products of 1.99, one of 0.996 a step
+    a[0], a[1] = 1.0, under * 2.0 ** -17
+    for delta in range(356, 380, 4) if d == 128 else range(176, 192, 4):
+        b = torch.full((d,), -under * 2.0 ** -14)
+        b[0], b[1] = 1.0, delta * 2.0 ** -17
+        sa, sb = (x.double() @ y.double() for y in (a, b))
+        # (delta less what B loses below what A adds up to)
+        want_a = bool(sa > sb)
+        for swap in (False, True):
+            c = torch.zeros(6, d)
+            c[:, 0] = 0.5
+            c[1], c[2] = (b, a) if swap else (a, b)
+            cb = c.to(BF).cuda()
+            assert torch.equal(cb.float().cpu(), c)
+            q = x.repeat(1, 3, 1).to(BF).cuda()
+            got = m.blasst_block_select(q[None], cb[None, None], 6 * 64,
+                                        n_sel=3, causal=False)
+            best = (1 if want_a else 2) if not swap else (2 if want_a else 1)
+            assert got[0, 0].tolist() == [[0, best, 5]] * 3, (delta, swap, n)
+    _clean(m)
