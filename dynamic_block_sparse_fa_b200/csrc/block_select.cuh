@@ -474,10 +474,10 @@ __device__ __forceinline__ bool take_row(const RowTask& r, ExactT exact) {
 // float64 score of block j.
 //
 // Blocks whose place a cut leaves open are scored again, as the distance of
-// their exact score to a reference among them, rounded to float32.  Rounding
-// keeps the order, so after another cut only blocks that tie there are open;
-// the next round takes the first of them as its reference, and the rounds end
-// when the tied blocks equal it in float64.
+// their exact score to a reference among them, rounded.  Rounding keeps the
+// order, so after another cut only blocks that tie there are open; the next
+// round takes the first of them as its reference, and the rounds end when the
+// tied blocks equal it in float64.
 template <class GroupT, class ExactT>
 __device__ void take_general(GroupT& g, float* s, const RowTask& r,
                              ExactT exact) {
@@ -512,8 +512,9 @@ __device__ void take_general(GroupT& g, float* s, const RowTask& r,
         todo &= todo - 1;
         const double e = exact(r.f + i0 + t) - ref;
         if (lane == t) {
-          y = (float)e;
-          if (y == 0.f && e != 0.0) y = copysignf(1e-45f, y);  // 0 is 0 only
+          // later rounds: exponent and 12 bits, float64's whole range
+          const int u = (int)(__double_as_longlong(fabs(e)) >> 40);
+          y = start ? (float)e : copysignf((float)u, (float)e);
           if (nan_only) y = 0.f;
           if (isnan(e)) y = -INFINITY;
         }
@@ -614,14 +615,32 @@ __device__ __forceinline__ bool fill_fixed(GroupT& g, const SelRange& r,
 template <int D>
 constexpr float kSelEpsMma = (D / 8) * 22 * 2.98023223876953125e-08f;  // 2^-25
 constexpr float kSelEpsFma = 3.814697265625e-06f;  // 2^-18
-// Norms of q are summed over values scaled by 2^40, so that squares of small
-// values stay above float32's smallest (a sum that overflows only sends the
-// row to the float64 scores).
+// Norms are summed over values scaled by 2^40 (the prompt kernel's means are
+// not), so that squares of small values stay above float32's smallest (a sum
+// that overflows only sends the row to the float64 scores).  What is still
+// smaller must not count as nothing: unless every value is 0 a squared norm
+// gets kNormFloor, far above what its squares can lose (128 of 2^-149).
 constexpr float kNormUp = 1099511627776.f, kNormDown = 1.f / 1099511627776.f;
+constexpr float kNormFloor = 4e-36f;
 
-// nw nc, for the norm nw of w and the largest norm nc of a mean; infinite
-// where the scores themselves may leave float32's range (w is at least 2^-18
-// of what they sum).
+// The largest squared norm of the means at c (n chunks of 16 bytes) from its
+// bits; whole CTA of NT threads.
+template <int NT>
+__device__ __forceinline__ float floor_norm(uint32_t bits,
+                                            const __nv_bfloat16* c, int n) {
+  if (bits >= __float_as_uint(kNormFloor)) return __uint_as_float(bits);
+  uint32_t nz = 0u;  // bits of every value but their signs
+  for (int e = threadIdx.x; e < n; e += NT) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(c) + e);
+    nz |= (w.x | w.y | w.z | w.w) & 0x7fff7fffu;
+  }
+  return __syncthreads_or(nz != 0u) ? kNormFloor : 0.f;
+}
+
+// nw nc, for the norm nw of w and the largest norm nc of a mean, but no less
+// than scores among float32's smallest numbers are off by; infinite where the
+// scores themselves may leave float32's range (w is at least 2^-18 of what
+// they sum); 0 where all are 0.
 __device__ __forceinline__ float score_eps(float nw, float nc) {
   const float e = nw * nc;
   if (!(e < 1e33f)) return INFINITY;
@@ -745,13 +764,14 @@ __global__ void __launch_bounds__(kSelDecThreads, 2)
     float qq = 0.f;
 #pragma unroll
     for (int x = 0; x < D / 32; ++x) {
-      const float y = qa[lane + 32 * x] * kNormUp;
-      qq = fmaf(y, y, qq);
+      const float y = qa[lane + 32 * x];
+      qq = fmaf(y * kNormUp, y * kNormUp, y > 0.f ? qq + kNormFloor : qq);
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) qq += __shfl_xor_sync(~0u, qq, o);
     eps = score_eps(kSelEpsFma * (sqrtf(qq) * kNormDown),
-                    sqrtf(__uint_as_float(cmax_s)) * kNormDown);
+                    sqrtf(floor_norm<kSelDecThreads>(
+                        cmax_s, c0 + (size_t)r.f * D, n * CH)) * kNormDown);
   }
   double qd[D / 32];
   bool have_q = false;
@@ -894,7 +914,8 @@ __global__ void __launch_bounds__(256, 3)
   {
     const __nv_bfloat16* q0 =
         a.q + ((size_t)b * a.Hkv + h) * (size_t)a.G * a.Lq * D;
-    const float head_eps = (float)(a.G - 1) * 5.9604644775390625e-08f;  // 2^-24
+    const float head_eps =
+        (float)(a.G - 1) * 5.9604644775390625e-08f * kNormUp;  // 2^-24, scaled
     for (int e = tid; e < TM * CH; e += 256) {
       const int row = e / CH, ch = e % CH;
       float x[8], y[8];
@@ -925,17 +946,16 @@ __global__ void __launch_bounds__(256, 3)
         ph[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
         pl[i] = pack_bf16x2(x[2 * i] - bf16lo(ph[i]),
                             x[2 * i + 1] - bf16hi(ph[i]));
-        // the error of these two columns, see kSelEpsMma
-        const float w0 = fmaf(kSelEpsMma<D>, fabsf(x[2 * i]),
-                              fmaf(head_eps, y[2 * i],
-                                   fabsf(x[2 * i] - bf16lo(ph[i]) - bf16lo(pl[i])))) *
-                         kNormUp;
-        const float w1 = fmaf(kSelEpsMma<D>, fabsf(x[2 * i + 1]),
-                              fmaf(head_eps, y[2 * i + 1],
-                                   fabsf(x[2 * i + 1] - bf16hi(ph[i]) - bf16hi(pl[i])))) *
-                         kNormUp;
+        // the error of these two columns, see kSelEpsMma, scaled
+        const float r0 = fabsf(x[2 * i] - bf16lo(ph[i]) - bf16lo(pl[i]));
+        const float r1 = fabsf(x[2 * i + 1] - bf16hi(ph[i]) - bf16hi(pl[i]));
+        const float w0 = fmaf(kSelEpsMma<D> * kNormUp, fabsf(x[2 * i]),
+                              fmaf(head_eps, y[2 * i], r0 * kNormUp));
+        const float w1 = fmaf(kSelEpsMma<D> * kNormUp, fabsf(x[2 * i + 1]),
+                              fmaf(head_eps, y[2 * i + 1], r1 * kNormUp));
         nn = fmaf(w0, w0, nn);
         nn = fmaf(w1, w1, nn);
+        if (y[2 * i] > 0.f || y[2 * i + 1] > 0.f) nn += kNormFloor;
       }
       uint8_t* dst = sq + row * C::QROW;
       *reinterpret_cast<uint4*>(dst + ((ch ^ (row & 7)) << 4)) =
@@ -1007,10 +1027,8 @@ __global__ void __launch_bounds__(256, 3)
     if (lane == 0) atomicMax(cmax_s, cw);
     __syncthreads();
   }
-  // (squares below float32's smallest normal number lose their digits: no
-  // norm counts as less than 2e-18 unless it is 0; NaN stays NaN)
-  float cmax = sqrtf(__uint_as_float(*cmax_s));
-  if (*cmax_s != 0u && cmax < 2e-18f) cmax = 2e-18f;
+  const float cmax =
+      sqrtf(floor_norm<256>(*cmax_s, c0, min(nct * kSelBlock, a.nblk) * CH));
   WarpGroup g;
   for (int rr = warp; rr < nrow; rr += 8) {
     const int row = row0 + rr;

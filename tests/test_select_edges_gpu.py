@@ -200,3 +200,15 @@ def test_select_scores_the_tensor_core_cuts_most(m, d):
             best = (1 if want_a else 2) if not swap else (2 if want_a else 1)
             assert got[0, 0].tolist() == [[0, best, 5]] * 3, (delta, swap, n)
     _clean(m)
+
+
+# ---------------------------------------------------- the small end of float32
+@pytest.mark.parametrize("fq,fc", [(1.0, 1e-20), (1.0, 1e-25), (1e-36, 1.0),
+                                   (1e-20, 1e-19), (1e-25, 1e-28)])
+def test_select_close_scores_of_small_values(m, fq, fc):
+    """Scores near and below float32's smallest numbers are still ranked by
+    their exact values."""
+    g = _gen(5)
+    q = _close_query(g, 2, 20, 128, fq)
+    _check_prompt(m, q, _close_means(g, 90, 128, fc), False, 20)
+    _check_one(m, q, _close_means(g, 300, 128, fc), 40)
