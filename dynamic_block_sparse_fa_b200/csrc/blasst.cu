@@ -1274,7 +1274,8 @@ blasst_status_t blasst_block_select(const void* q, const void* means, int* sel,
     return BLASST_ERR_INVALID_ARG;
   if (!select_slots_ok(n_sel, n_first, n_local)) return BLASST_ERR_INVALID_ARG;
   if (causal && (Lq > Lkv || n_local < 1)) return BLASST_ERR_INVALID_ARG;
-  if (!select_dim_ok(d) || Hq / Hkv > 32 || Lkv > 131072 || n_sel > 4096)
+  if (!select_dim_ok(d) || Hq / Hkv > 32 || n_sel > 4096 ||
+      Lkv > blasst::kSelPromptMaxBlocks * blasst::kSelBlock)
     return BLASST_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(q) || !aligned16(means)) return BLASST_ERR_MISALIGNED;
   blasst::SelectArgs a;
@@ -1311,7 +1312,8 @@ blasst_status_t blasst_block_select_decode(const void* q, const void* means,
   const long long nblk =
       ((long long)max_seq_len + blasst::kSelBlock - 1) / blasst::kSelBlock;
   if (nblk > max_blocks) return BLASST_ERR_INVALID_ARG;
-  if (!select_dim_ok(d) || Hq / Hkv > 32 || nblk > 16384 || n_sel > 4096 ||
+  if (!select_dim_ok(d) || Hq / Hkv > 32 ||
+      nblk > blasst::kSelDecMaxBlocks || n_sel > 4096 ||
       (long long)B * Hkv > 0x7fffffffLL)
     return BLASST_ERR_UNSUPPORTED_SHAPE;
   if (!aligned16(q) || !aligned16(means)) return BLASST_ERR_MISALIGNED;

@@ -670,6 +670,7 @@ __device__ __forceinline__ double exact_score(const double (&qd)[D / 32],
 // doubtful blocks (2).
 // ---------------------------------------------------------------------------
 constexpr int kSelDecThreads = 512;
+constexpr int kSelDecMaxBlocks = 16384;  // their scores fill 64 KB
 
 template <int D>
 __global__ void __launch_bounds__(kSelDecThreads, 2)
@@ -814,9 +815,11 @@ template <int D>
 cudaError_t launch_block_select_decode(const SelectArgs& a, int B, int nblk,
                                        cudaStream_t st) {
   const int smem = nblk * 4;
+  // (the limit is the function's, shared by every thread of the process: the
+  // same for all calls, so that none takes back what another relies on)
   cudaError_t e = cudaFuncSetAttribute(
       block_select_decode_kernel<D>,
-      cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      cudaFuncAttributeMaxDynamicSharedMemorySize, kSelDecMaxBlocks * 4);
   if (e != cudaSuccess) return e;
   block_select_decode_kernel<D>
       <<<(unsigned)(B * a.Hkv), kSelDecThreads, smem, st>>>(a);
@@ -856,6 +859,7 @@ __device__ __forceinline__ void cp_async_wait_but_one() {
 }
 
 constexpr int kSelRows = 16;  // rows per CTA
+constexpr int kSelPromptMaxBlocks = 2048;  // 16 rows' scores fill 128 KB
 
 template <int D>
 struct SelectCfg {
@@ -1072,18 +1076,20 @@ __global__ void __launch_bounds__(256, 3)
 
 // Score columns kept per row: whole 64-block tiles, plus 8 floats so that the 8
 // rows a fragment store writes fall into different banks.
-inline int select_ld(int nblk) { return (nblk + 63) / 64 * 64 + 8; }
+constexpr int select_ld(int nblk) { return (nblk + 63) / 64 * 64 + 8; }
 
 template <int D>
 cudaError_t launch_block_select(SelectArgs a, int B, cudaStream_t st) {
   a.ld = select_ld(a.nblk);
   a.ntile = (a.Lq + kSelRows - 1) / kSelRows;
   const int smem = SelectCfg<D>::smem(a.ld);
+  constexpr int most = SelectCfg<D>::smem(select_ld(kSelPromptMaxBlocks));
+  static_assert(most <= 232448, "shared memory per CTA");
   const long long grid = (long long)a.ntile * B * a.Hkv;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(
       block_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-      smem);
+      most);  // (of all calls, as above)
   if (e != cudaSuccess) return e;
   block_select_kernel<D><<<(unsigned)grid, 256, smem, st>>>(a);
   return cudaGetLastError();

@@ -663,8 +663,10 @@ inline cudaError_t launch_select_lists(SelListArgs* a, const int* sel,
   const long long grid = (long long)BH * a->ntile;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const int smem = gm.nblk * gm.wpt * 4;
+  // the limit of all calls: it is the function's, shared by every thread
   cudaError_t e = cudaFuncSetAttribute(
-      select_lists_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      select_lists_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      kSelMaxBlocks * 4 * 4);
   if (e != cudaSuccess) return e;
   select_lists_kernel<<<(unsigned)grid, 256, smem, st>>>(*a);
   return cudaGetLastError();

@@ -4,6 +4,7 @@ Selections are whole numbers and have to be equal.  Other tolerances are
 derived where they are used.
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -212,3 +213,76 @@ def test_select_close_scores_of_small_values(m, fq, fc):
     q = _close_query(g, 2, 20, 128, fq)
     _check_prompt(m, q, _close_means(g, 90, 128, fc), False, 20)
     _check_one(m, q, _close_means(g, 300, 128, fc), 40)
+
+
+# --------------------------------------------------------------- host threads
+def _threads(calls, n):
+    """Each C call n times on a host thread and stream of its own, all at once;
+    a call is a function and its arguments but the stream."""
+    failed = []
+    start = threading.Barrier(len(calls))
+
+    def loop(fn, args, stream):
+        start.wait()
+        for i in range(n):
+            st = fn(*args, stream)
+            if st:
+                failed.append((fn.__name__, i, st))
+                return
+            if i % 256 == 255:      # bounds the launches in flight
+                torch.cuda.current_stream().synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    ts = [threading.Thread(target=loop, args=(*c, s.cuda_stream))
+          for c, s in zip(calls, streams)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+
+
+@pytest.mark.parametrize("op", ["select", "select_decode", "prefill"])
+def test_threads_with_different_lengths(m, op):
+    """Host threads on the longest sequences beside others on short ones:
+    none may disturb another's launch."""
+    lib = m.blasst._lib
+    g = _gen(1)
+    keep = []               # what the raw pointers below point to
+
+    def ptr(t):
+        keep.append(t)
+        return t.data_ptr()
+
+    def make(L):
+        if op == "select":
+            out = torch.zeros(16, 3, dtype=torch.int32, device="cuda")
+            return out, (lib.blasst_block_select, (
+                ptr(_rand(g, 16, 64)), ptr(_rand(g, R.nblk(L), 64)), ptr(out),
+                1, 1, 1, 16, L, 64, 0, 3, 1, 1))
+        if op == "select_decode":
+            out = torch.zeros(1, 3, dtype=torch.int32, device="cuda")
+            ln = torch.tensor([L], dtype=torch.int32, device="cuda")
+            return out, (lib.blasst_block_select_decode, (
+                ptr(_rand(g, 1, 64)), ptr(_rand(g, R.nblk(L), 64)), ptr(ln), L,
+                R.nblk(L), ptr(out), 1, 1, 1, 64, 3, 1, 1))
+        out = torch.zeros(8, 64, dtype=BF, device="cuda")
+        n = m.blasst_select_prefill_workspace_size(1, 1, 1, 8, L)
+        ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        sel = torch.zeros(8, 1, dtype=torch.int32, device="cuda")
+        return out, (lib.blasst_select_prefill, (
+            ptr(_rand(g, 8, 64)), ptr(_rand(g, L, 64)), ptr(_rand(g, L, 64)),
+            ptr(sel), ptr(out), None, 1, 1, 1, 8, L, 64, 1, 0.1, 0, ptr(ws), n))
+    L = {"select": 131072, "select_decode": 1 << 20, "prefill": 262144}[op]
+    work = [make(L), make(640), make(64), make(L), make(1), make(640)]
+    for out, (fn, args) in work:
+        assert fn(*args, None) == 0
+    torch.cuda.synchronize()
+    want = [out.clone() for out, _ in work]
+    for out, _ in work:
+        out.zero_()
+    torch.cuda.synchronize()
+    _threads([call for _, call in work], 4000)
+    _clean(m)
+    for (out, _), w in zip(work, want):
+        assert torch.equal(out, w)
