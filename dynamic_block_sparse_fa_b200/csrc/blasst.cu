@@ -1185,6 +1185,23 @@ bool select_dim_ok(int d) { return d == 64 || d == 128; }
 // tokens fill whole 16-byte rows of the backward's lse and D boxes.
 bool select_group_ok(int G) { return G >= 1 && G <= 32 && (G & (G - 1)) == 0; }
 
+// Whether an output's bytes meet a page of a pool: num_pages pages of `page`
+// elements, page_stride apart.  (Between pages further apart than their rows
+// there is room for other things.)
+bool on_pages(const void* out, size_t bytes, const void* pool, int num_pages,
+              long long page_stride, long long page) {
+  if (!out) return false;
+  // from the pool's first byte, as 64-bit differences
+  const long long a0 = (long long)(reinterpret_cast<uintptr_t>(out) -
+                                   reinterpret_cast<uintptr_t>(pool));
+  const long long a1 = a0 + (long long)bytes;
+  if (a1 <= 0) return false;
+  const long long step = 2 * page_stride, n = 2 * page;
+  // the first page that ends behind a0
+  const long long i = a0 < n ? 0 : (a0 - n) / step + 1;
+  return i < num_pages && i * step < a1;
+}
+
 bool select_slots_ok(int n_sel, int n_first, int n_local) {
   return n_sel >= 1 && n_first >= 0 && n_local >= 0 &&
          (long long)n_first + n_local <= n_sel;
@@ -1235,6 +1252,9 @@ blasst_status_t blasst_block_means_paged(
   if (page_stride < (long long)Hkv * page_size * d || page_stride % 8 != 0)
     return BLASST_ERR_INVALID_ARG;
   if (!aligned16(k_pages) || !aligned16(means)) return BLASST_ERR_MISALIGNED;
+  if (on_pages(means, (size_t)B * Hkv * max_blocks * d * 2, k_pages, num_pages,
+               page_stride, (long long)Hkv * page_size * d))
+    return BLASST_ERR_INVALID_ARG;
   blasst::MeansArgs a;
   memset(&a, 0, sizeof a);
   a.k = static_cast<const __nv_bfloat16*>(k_pages);
@@ -1519,6 +1539,13 @@ blasst_status_t blasst_select_decode_paged(
   const blasst_status_t ws = carve_workspace(workspace, workspace_bytes, B, Hq,
                                              d, S, &m.o_part, &m.lse_part);
   if (ws != BLASST_OK) return ws;
+  const long long page = (long long)Hkv * page_size * d;
+  for (const void* pool : {k_pages, v_pages})
+    if (on_pages(o, (size_t)B * Hq * d * 2, pool, num_pages, page_stride, page) ||
+        on_pages(lse, (size_t)B * Hq * 4, pool, num_pages, page_stride, page) ||
+        on_pages(workspace, blasst_decode_workspace_size(B, Hq, d, S), pool,
+                 num_pages, page_stride, page))
+      return BLASST_ERR_INVALID_ARG;
   if (!encode_pool_maps(&m, k_pages, v_pages, d, page_size, Hkv, num_pages,
                         page_stride, page_size < 64 ? page_size : 64))
     return cuda_status(cudaErrorInvalidValue, "selected decode tensor maps");

@@ -551,7 +551,7 @@ blasst_status_t blasst_block_means(const void *k, void *means, int B, int Hkv,
  *  means       device bf16 [B,Hkv,max_blocks,d]; other blocks, those past a
  *              sequence's end among them, are left as they are
  *  max_blocks  >= ceil(max_seq_len / 64)
- * A bad length or page id is recorded as in blasst_decode_paged, and the mean
+ * means may not overlap a page of the pool (refused).  A bad length or page id is recorded as in blasst_decode_paged, and the mean
  * it belongs to is not written.
  */
 blasst_status_t blasst_block_means_paged(
@@ -657,7 +657,8 @@ blasst_status_t blasst_select_prefill_backward(
  *  num_splits  1 .. n_sel, or 0 = blasst_select_decode_splits
  *  workspace   blasst_decode_workspace_size(B, Hq, d, resolved num_splits)
  * Only the pages of selected blocks are read; their table entries are checked
- * on the device as in blasst_decode_paged.
+ * on the device as in blasst_decode_paged.  o, lse and the workspace may not
+ * overlap a page of the pools (refused).
  */
 blasst_status_t blasst_select_decode_paged(
     const void *q, const void *k_pages, const void *v_pages,
