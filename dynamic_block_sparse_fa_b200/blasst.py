@@ -772,11 +772,17 @@ _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 def _on_stream(fn):
     """stream=s runs the call as under torch.cuda.stream(s): what it allocates
-    (outputs, workspace) then belongs to that stream too."""
+    (outputs, workspace) then belongs to that stream too.  s has to be a stream
+    of the tensors' device: torch.cuda.stream(s) leaves another device's current
+    stream as it is, and the call would run on that one."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
         if stream is None:
             return fn(*args, **kw)
+        for t in (*args, *kw.values()):
+            if isinstance(t, torch.Tensor) and t.device != stream.device:
+                raise ValueError(f"stream: on {stream.device}, a tensor is on "
+                                 f"{t.device}")
         with torch.cuda.stream(stream):
             return fn(*args, **kw)
     return call

@@ -84,3 +84,21 @@ def test_outputs_may_not_lie_in_the_cache():
                                pool[3, 0, 0, :2].view(1, 1, 2, 128))
     torch.cuda.synchronize()
     assert m.blasst_check_device_error()[0] == 0
+
+
+def test_stream_of_another_device_is_refused():
+    import dynamic_block_sparse_fa_b200 as m
+
+    class Other:                      # a stream of a second GPU
+        device = torch.device("cuda", 1)
+    dev = "cuda" if torch.cuda.is_available() else "cpu"
+    k = torch.zeros(1, 1, 64, 128, dtype=torch.bfloat16, device=dev)
+    sel = torch.zeros(1, 1, 64, 1, dtype=torch.int32, device=dev)
+    for call in (lambda: m.blasst_block_means(k, stream=Other()),
+                 lambda: m.blasst_block_select(q=k, means=k[:, :, :1],
+                                               Lkv=64, n_sel=1,
+                                               stream=Other()),
+                 lambda: m.blasst_select_prefill(k, k, k, sel,
+                                                 stream=Other())):
+        with pytest.raises(ValueError, match="stream: on cuda:1"):
+            call()
