@@ -286,3 +286,51 @@ def test_threads_with_different_lengths(m, op):
     _clean(m)
     for (out, _), w in zip(work, want):
         assert torch.equal(out, w)
+
+
+# -------------------------------------------------- streams, graphs, same bits
+def _step(m, q, k, v, do, n_sel):
+    c = m.blasst_block_means(k)
+    sel = m.blasst_block_select(q, c, k.shape[2], n_sel=n_sel, n_local=2)
+    o, lse = m.blasst_select_prefill(q, k, v, sel)
+    return (c, sel, o, lse) + tuple(m.blasst_select_prefill_backward(
+        q, k, v, o, lse, do, sel))
+
+
+def test_training_steps_have_the_same_bits_everywhere(m):
+    """Every output, dq among them, sums in a fixed order: two streams at once,
+    a side stream and a replayed graph give what one call alone gave."""
+    g = _gen(70)
+    ins = []
+    for L in (400, 1100):
+        ins.append((_rand(g, 1, 8, L, 128), _rand(g, 1, 2, L, 128),
+                    _rand(g, 1, 2, L, 128), _rand(g, 1, 8, L, 128), 5))
+    want = []
+    for x in ins:
+        want.append(_step(m, *x))
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    graphs, captured = [], []
+    for x in ins:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            captured.append(_step(m, *x))
+    for _ in range(5):
+        got = [None, None]
+        for i, s in enumerate(streams):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got[i] = _step(m, *ins[i])
+        torch.cuda.synchronize()
+        for outs in captured:
+            for t in outs:
+                t.zero_()
+        torch.cuda.synchronize()
+        for i, s in enumerate(streams):     # both graphs at once
+            with torch.cuda.stream(s):
+                graphs[i].replay()
+        torch.cuda.synchronize()
+        for a, b, w in zip(got, captured, want):
+            for name, x, y, z in zip("c sel o lse dq dk dv".split(), a, b, w):
+                assert torch.equal(x, z) and torch.equal(y, z), name
+    _clean(m)
