@@ -607,13 +607,16 @@ __device__ __forceinline__ bool fill_fixed(GroupT& g, const SelRange& r,
 // B200 cuts each of the 17 to a multiple of 2^-25 of the largest one's power
 // of two and the result to 24 bits (seen on sums that tell; always towards
 // zero).  With |x| |c| above every partial sum a step is off by at most
-// (17 + 4) 2^-25 |x| |c|, and there are 2 d / 16; the 22nd part covers the
-// roundings of the norms.  (Half the bound, 2^-18, was wrong on sums built to
-// lose most.)
+// (17 + 4) 2^-25 |x| |c|.  The large parts' sum takes d / 16 steps; the small
+// parts, 2^-8 of them, are summed apart, so that their steps cut 2^-8 of that;
+// in one sum they would double the bound.  (16K prompt, 32 heads on 8: 202 us
+// apart and 200 in one; 232 and 242 where the means share a direction 30 times
+// their spread and more rows have doubtful blocks.)  The 22nd part covers them
+// and the roundings of the norms.
 // CUDA cores (no split): the head sum 2^-19 sum_g |q_g| for G <= 32, and 13
 // roundings of 2^-24 in the dot product: below 2^-18 sum_g |q_g|.
 template <int D>
-constexpr float kSelEpsMma = (D / 8) * 22 * 2.98023223876953125e-08f;  // 2^-25
+constexpr float kSelEpsMma = (D / 16) * 22 * 2.98023223876953125e-08f;  // 2^-25
 constexpr float kSelEpsFma = 3.814697265625e-06f;  // 2^-18
 // Norms are summed over values scaled by 2^40 (the prompt kernel's means are
 // not), so that squares of small values stay above float32's smallest (a sum
@@ -639,11 +642,11 @@ __device__ __forceinline__ float floor_norm(uint32_t bits,
 
 // nw nc, for the norm nw of w and the largest norm nc of a mean, but no less
 // than scores among float32's smallest numbers are off by; infinite where the
-// scores themselves may leave float32's range (w is at least 2^-18 of what
+// scores themselves may leave float32's range (w is at least 2^-19 of what
 // they sum); 0 where all are 0.
 __device__ __forceinline__ float score_eps(float nw, float nc) {
   const float e = nw * nc;
-  if (!(e < 1e33f)) return INFINITY;
+  if (!(e < 5e32f)) return INFINITY;
   return nw > 0.f && nc > 0.f ? fmaxf(e, 1e-37f) : 0.f;
 }
 
@@ -998,7 +1001,8 @@ __global__ void __launch_bounds__(256, 3)
     const uint32_t ca = smem_u32(sc + (ct & 1) * C::CBYTES);
     // The scores, and the largest |c|^2 among the tile's blocks: the diagonal
     // of c c^T (a row-major A fragment of 8 rows is their B fragment).
-    float acc[4] = {0.f, 0.f, 0.f, 0.f}, d0 = 0.f, d1 = 0.f;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, low[4] = {0.f, 0.f, 0.f, 0.f};
+    float d0 = 0.f, d1 = 0.f;
 #pragma unroll
     for (int p = 0; p < KST / 2; ++p) {
       const int row = warp * 8 + mr;
@@ -1006,9 +1010,9 @@ __global__ void __launch_bounds__(256, 3)
       ldsm_x4(ca + row * (D * 2) + (((4 * p + mi) ^ (row & 7)) << 4), r0, r1, r2,
               r3);
       mma16816(acc, ah[2 * p], r0, r1);
-      mma16816(acc, al[2 * p], r0, r1);
+      mma16816(low, al[2 * p], r0, r1);
       mma16816(acc, ah[2 * p + 1], r2, r3);
-      mma16816(acc, al[2 * p + 1], r2, r3);
+      mma16816(low, al[2 * p + 1], r2, r3);
       mma16816_top(d0, d1, r0, r1, r0, r1);
       mma16816_top(d0, d1, r2, r3, r2, r3);
     }
@@ -1016,8 +1020,10 @@ __global__ void __launch_bounds__(256, 3)
       const int col = ct * kSelBlock + warp * 8 + 2 * (lane & 3);
       const int row = lane >> 2;
 #pragma unroll
-      for (int x = 0; x < 4; ++x)
+      for (int x = 0; x < 4; ++x) {
+        acc[x] += low[x];
         if (isnan(acc[x])) acc[x] = -INFINITY;
+      }
       *reinterpret_cast<float2*>(S + (size_t)row * a.ld + col) =
           make_float2(acc[0], acc[1]);
       *reinterpret_cast<float2*>(S + (size_t)(row + 8) * a.ld + col) =
