@@ -10,13 +10,14 @@
 //                       rows) any of whose tokens selected either half
 //   select_dq_kernel    a CTA keeps one query tile and streams the 64-key
 //                       blocks its tokens selected, two a step
-// That is 4 + 3 products of 128^3 a pair where one pass over the pairs needs
-// 5, but the one pass has to add every pair's dQ tile (64 KB of float32) to
-// memory: at 8K causal, 32 heads on 8, 16 blocks a row, the additions alone
-// cost 370 of its 1190 us, they leave the tensor memory no
-// room to overlap the products with the threads' work, and their order
-// changes the result from run to run.  The dQ pass also walks 64-key blocks,
-// a third fewer than the 128-key pairs.  Both passes sum in a fixed order.
+// One pass over the pairs would need 5 products of 128^3 for each where these
+// need 4 and 3 (and 2 more for the dQ pass's accuracy, see there), but it has
+// to add every pair's dQ tile (64 KB of float32) to memory: at 8K causal, 32
+// heads on 8, 16 blocks a row, the additions alone cost 370 of its 1190 us,
+// they leave the tensor memory no room to overlap the products with the
+// threads' work, and their order changes the result from run to run.  The dQ
+// pass also walks 64-key blocks, a third fewer than the 128-key pairs.  Both
+// passes sum in a fixed order.  The dQ pass runs first: it corrects D.
 //
 // Before them:
 //   select_prep_kernel   -D and -lse * log2 e per query row
@@ -185,7 +186,7 @@ constexpr int kSelBwdThreads = 64 + 256;  // producer, issuer, 8 compute warps
 //   [P_n written] dV_n, S^T_{n+1}   [dS_n written] dK_n, dP^T_{n+1}
 // so that the threads' dS_n overlaps dV_n and S^T_{n+1}, and their P_{n+1}
 // overlaps dK_n and dP^T_{n+1}.  8K causal, 32 heads on 8, 16 blocks a row
-// (38.6k pairs): 0.52 ms, the tensor pipe 60% busy; what bounds a pair is the
+// (38.6k pairs): 0.53 ms, the tensor pipe 58% busy; what bounds a pair is the
 // hand-offs between its products and the threads' two phases.
 // ---------------------------------------------------------------------------
 template <bool V>
@@ -594,15 +595,23 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// dQ.  Per step of two 64-key blocks three products, a thread is a query row:
+// dQ.  Per step of two 64-key blocks five products, a thread is a query row:
 //   S = Q K_s^T -> TMEM [0, 128)    dP = dO V_s^T -> [128, 256)
-//   dQ += dS K_s -> [256, 384), dS the bf16 A operand in one of two buffers
-//         [384, 448), [448, 512)
-// The issuer's order per step is
-//   [S_s read] S_{s+1}   [dS_s written, so dP_s read] dP_{s+1}, dQ_s
-// and the threads' exps of step s+1 overlap dP_{s+1}, their dS_{s+1} overlaps
-// dQ_s.  K_s is needed until dQ_s: three K slots, two V slots.  The same 8K
-// case (25k steps): 0.27 ms, the tensor pipe 55% busy.
+//   dQ += dS K_s -> [256, 384)      M += P K_s -> [384, 512)
+// The gradient is scale sum_c dS_c k_c, and two roundings in it are large
+// beside that of the result (2^-9 of it on average): dS as one bf16 operand
+// (as much again), and D = dO . o from the bf16 o, whose error dD adds
+// dD sum_c P_c k_c to a row.  So dS goes in as two bf16 parts (two of the five
+// products), and the row sum of dS, 0 with the right D, gives dD: it is
+// subtracted with M at the end, and the dK, dV pass behind this one gets the
+// corrected D.  dQ's error is then its rounding, 0.0017 of its norm, where it
+// was 0.0028 to 0.0038, the more the fewer keys a row has.  P and dS are the A operands, written over
+// the S and dP they come from.  The issuer's order is
+//   [P_s written] M_s, S_{s+1}   [dS_s written] dQ_s, dP_{s+1}
+// so that the threads' dS_s overlaps M_s and S_{s+1}, and their P_{s+1}
+// overlaps dQ_s and dP_{s+1}.  K_s is needed until dQ_s: three K slots, two V
+// slots.  The same 8K case (25k steps): 0.37 ms, the tensor pipe 69% busy; with
+// three products (dS one part, no M) 0.27 ms at 55%.
 // ---------------------------------------------------------------------------
 struct SelDqCfg {
   static constexpr int TILE = 128 * kBwdD * 2;
@@ -612,15 +621,16 @@ struct SelDqCfg {
   static constexpr int OFF_DO = OFF_Q + TILE;
   static constexpr int OFF_K = OFF_DO + TILE;
   static constexpr int OFF_V = OFF_K + NKS * TILE;
-  static constexpr int OFF_BAR = OFF_V + NVS * TILE;
+  static constexpr int OFF_R = OFF_V + NVS * TILE;  // f32 [2][128] sums of dS
+  static constexpr int OFF_BAR = OFF_R + 2 * 128 * 4;
   static constexpr int B_Q = 0;
   static constexpr int B_KF = 1;           // [3]
   static constexpr int B_KE = B_KF + NKS;  // [3]
   static constexpr int B_VF = B_KE + NKS;  // [2]
   static constexpr int B_VE = B_VF + NVS;  // [2]
   static constexpr int B_SF = B_VE + NVS;  // S in TMEM
-  static constexpr int B_SR = B_SF + 1;    // S read (one arrival per warp)
-  static constexpr int B_DPF = B_SR + 1;   // dP in TMEM
+  static constexpr int B_PR = B_SF + 1;    // P written (one arrival per warp)
+  static constexpr int B_DPF = B_PR + 1;   // dP in TMEM
   static constexpr int B_DSR = B_DPF + 1;  // dS written (one per warp)
   static constexpr int B_OD = B_DSR + 1;
   static constexpr int B_DR = B_OD + 1;    // drain after a wait gave up
@@ -664,7 +674,7 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
       mbar_init(&bar[C::B_VE + i], 1);
     }
     mbar_init(&bar[C::B_SF], 1);
-    mbar_init(&bar[C::B_SR], 8);
+    mbar_init(&bar[C::B_PR], 8);
     mbar_init(&bar[C::B_DPF], 1);
     mbar_init(&bar[C::B_DSR], 8);
     mbar_init(&bar[C::B_OD], 1);
@@ -764,15 +774,25 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
         mma_commit_elect(&bar[C::B_DPF]);
         mma_commit_elect(&bar[C::B_VE]);
       }
+      // D += A B, A 128 keys of bf16 in tensor memory: step k is 8 columns,
+      // steps 4 .. 7 64 columns on (block h of a step's two writes at 64 h)
+      auto mm_ts = [&](uint32_t d, uint32_t a0, uint64_t b0, bool first) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_ts_elect(d, a0 + (k >> 2) * 64 + (k & 3) * 8,
+                       b0 + (uint64_t)((k * 2048) >> 4), id_km,
+                       (first && k == 0) ? 0u : 1u);
+      };
       int k0 = 0;  // K slot of step s
       for (int s = 0; s < ns && ok; ++s) {
         const bool more = s + 1 < ns;
         const int k1 = k0 + 1 == C::NKS ? 0 : k0 + 1;
+        if (more) wait(C::B_KF + k1, ((s + 1) / C::NKS) & 1, s, 543);
+        wait(C::B_PR, s & 1, s, 544);
+        if (!ok) break;
+        tc_fence_after();
+        mm_ts(tmem + 384, tmem, dKm + k0 * kSlot, s == 0);
         if (more) {
-          wait(C::B_KF + k1, ((s + 1) / C::NKS) & 1, s, 543);
-          wait(C::B_SR, s & 1, s, 544);
-          if (!ok) break;
-          tc_fence_after();
           mm_ss(tmem, dQ, dKk + k1 * kSlot);
           mma_commit_elect(&bar[C::B_SF]);
           wait(C::B_VF + ((s + 1) & 1), ((s + 1) >> 1) & 1, s, 545);
@@ -780,17 +800,14 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
         wait(C::B_DSR, s & 1, s, 546);
         if (!ok) break;
         tc_fence_after();
+        mm_ts(tmem + 256, tmem + 128, dKm + k0 * kSlot, s == 0);
+        mm_ts(tmem + 256, tmem + 160, dKm + k0 * kSlot, false);
+        mma_commit_elect(&bar[C::B_KE + k0]);
         if (more) {
           mm_ss(tmem + 128, dO, dV + ((s + 1) & 1) * kSlot);
           mma_commit_elect(&bar[C::B_DPF]);
           mma_commit_elect(&bar[C::B_VE + ((s + 1) & 1)]);
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ts_elect(tmem + 256, tmem + 384 + (s & 1) * 64 + k * 8,
-                       dKm + k0 * kSlot + (uint64_t)((k * 2048) >> 4), id_km,
-                       (s > 0 || k > 0) ? 1u : 0u);
-        mma_commit_elect(&bar[C::B_KE + k0]);
         k0 = k1;
       }
       if (ok)
@@ -814,8 +831,10 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
         p.words + (slot * p.cap + h) * (size_t)p.wpt + (tt >> 5);
     const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
     const float sl2 = p.scale * kPrefLog2e;
-    const float ndel = active ? __ldg(p.delta + (size_t)(zq + g) * p.Lqp + tok) : 0.f;
+    float* del = p.delta + (size_t)(zq + g) * p.Lqp + tok;
+    const float ndel = active ? *del : 0.f;
     const float nl2 = active ? __ldg(p.lse2 + (size_t)(zq + g) * p.Lqp + tok) : 0.f;
+    float r0 = 0.f, r1 = 0.f;  // sum of this thread's dS
     bool ok = true;
     uint2 e_n = make_uint2(0, 0);
     unsigned w_n = 0;
@@ -840,10 +859,7 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
       tmem_ld32(lane_base + h * 64, sv[0]);
       tmem_ld32(lane_base + h * 64 + 32, sv[1]);
       tc_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar[C::B_SR]);
-      // P in place of S
+      // P in place of S, float32 here and bf16 for M
       const bool plain = __all_sync(FULL, nv <= 0 || nv >= kSelBlock);
       const bool on = nv > 0;
 #pragma unroll
@@ -865,27 +881,48 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
           for (int x = 0; x < 32; ++x)
             if (c * 32 + x >= nv) sv[c][x] = 0u;
       }
-      // dS = P o (dP - D), bf16, into the step's buffer (free: the commit of
-      // this dP followed the product that last read it)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        uint32_t st[16];
+#pragma unroll
+        for (int x = 0; x < 32; x += 2)
+          st[x >> 1] = pack_bf16x2(__uint_as_float(sv[c][x]),
+                                   __uint_as_float(sv[c][x + 1]));
+        tmem_st16(lane_base + h * 64 + c * 16, st);
+      }
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar[C::B_PR]);
       w = mbar_wait(&bar[C::B_DPF], s & 1, kWaitSelect, s, 551);
       ok = __all_sync(FULL, w);
       if (!ok) break;
       tc_fence_after();
+      // dS = P o (dP - D) over dP: its bf16 value in the first 32 of this
+      // thread's 64 columns, bf16 of what that leaves (off by 2^-16 of dS) in
+      // the others, those of the first keys behind the load of the second
+      const uint32_t col = lane_base + 128 + h * 64;
+      uint32_t lo[16];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         uint32_t dp[32], st[16];
-        tmem_ld32(lane_base + 128 + h * 64 + c * 32, dp);
+        tmem_ld32(col + c * 32, dp);
         tc_wait_ld();
+        if (c == 1) tmem_st16(col + 32, lo);
 #pragma unroll
         for (int x = 0; x < 32; x += 2) {
           float s0, s1;
           add_mul2(s0, s1, __uint_as_float(sv[c][x]),
                    __uint_as_float(sv[c][x + 1]), __uint_as_float(dp[x]),
                    __uint_as_float(dp[x + 1]), ndel, ndel);
-          st[x >> 1] = pack_bf16x2(s0, s1);
+          add2(r0, r1, s0, s1);
+          const uint32_t hi = pack_bf16x2(s0, s1);
+          st[x >> 1] = hi;
+          lo[x >> 1] = pack_bf16x2(s0 - bf16lo(hi), s1 - bf16hi(hi));
         }
-        tmem_st16(lane_base + 384 + (s & 1) * 64 + h * 32 + c * 16, st);
+        tmem_st16(col + c * 16, st);
       }
+      tmem_st16(col + 48, lo);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -896,28 +933,41 @@ __global__ void __launch_bounds__(kSelBwdThreads, 1)
       ok = __all_sync(FULL, w);
       tc_fence_after();
     }
+    // the row's sum of dS, from both its threads: what D was off by
+    float* rs = reinterpret_cast<float*>(smem + C::OFF_R) + rr;
+    rs[h * 128] = r0 + r1;
+    ok = named_sync_and(1 + quad, 64, ok);
     if (ok) {
+      const float r = rs[0] + rs[128];
+      if (active && h == 0 && fabsf(r) < INFINITY) *del = ndel - r;
       __nv_bfloat16* out =
           p.dq + ((size_t)(zq + g) * p.Lq + tok) * kBwdD + h * 64;
 #pragma unroll 1
       for (int c = 0; c < 2; ++c) {
-        uint32_t a[32];
+        uint32_t a[32], b2[32];
         if (ns > 0) {
           tmem_ld32(lane_base + 256 + h * 64 + c * 32, a);
+          tmem_ld32(lane_base + 384 + h * 64 + c * 32, b2);
           tc_wait_ld();
         } else {  // nothing selected
 #pragma unroll
-          for (int x = 0; x < 32; ++x) a[x] = 0u;
+          for (int x = 0; x < 32; ++x) a[x] = b2[x] = 0u;
         }
         if (active) {
 #pragma unroll
           for (int x = 0; x < 32; x += 8) {
-            uint4 w;
-            w.x = pack_bf16x2(__uint_as_float(a[x]) * p.scale, __uint_as_float(a[x + 1]) * p.scale);
-            w.y = pack_bf16x2(__uint_as_float(a[x + 2]) * p.scale, __uint_as_float(a[x + 3]) * p.scale);
-            w.z = pack_bf16x2(__uint_as_float(a[x + 4]) * p.scale, __uint_as_float(a[x + 5]) * p.scale);
-            w.w = pack_bf16x2(__uint_as_float(a[x + 6]) * p.scale, __uint_as_float(a[x + 7]) * p.scale);
-            *reinterpret_cast<uint4*>(out + c * 32 + x) = w;
+            uint32_t v[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              float q0, q1;
+              fma2v(q0, q1, __uint_as_float(b2[x + 2 * y]),
+                    __uint_as_float(b2[x + 2 * y + 1]), -r,
+                    __uint_as_float(a[x + 2 * y]),
+                    __uint_as_float(a[x + 2 * y + 1]));
+              v[y] = pack_bf16x2(q0 * p.scale, q1 * p.scale);
+            }
+            *reinterpret_cast<uint4*>(out + c * 32 + x) =
+                make_uint4(v[0], v[1], v[2], v[3]);
           }
         }
       }
@@ -1077,21 +1127,22 @@ inline cudaError_t launch_select_backward(const SelBwdProblem& pr,
   select_prep_kernel<<<(unsigned)prep_blocks, 256, 0, st>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(select_dkdv_kernel,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           SelDkdvCfg::SMEM_ALLOC);
-  if (e != cudaSuccess) return e;
-  select_dkdv_kernel
-      <<<(unsigned)slots, kSelBwdThreads, SelDkdvCfg::SMEM_ALLOC, st>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-
+  // (dQ first: it corrects the rows' D)
   e = cudaFuncSetAttribute(select_dq_kernel,
                            cudaFuncAttributeMaxDynamicSharedMemorySize,
                            SelDqCfg::SMEM_ALLOC);
   if (e != cudaSuccess) return e;
   select_dq_kernel
       <<<(unsigned)tiles, kSelBwdThreads, SelDqCfg::SMEM_ALLOC, st>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+
+  e = cudaFuncSetAttribute(select_dkdv_kernel,
+                           cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           SelDkdvCfg::SMEM_ALLOC);
+  if (e != cudaSuccess) return e;
+  select_dkdv_kernel
+      <<<(unsigned)slots, kSelBwdThreads, SelDkdvCfg::SMEM_ALLOC, st>>>(p);
   return cudaGetLastError();
 }
 

@@ -632,8 +632,10 @@ blasst_status_t blasst_select_prefill(const void *q, const void *k,
  *  d = 128; other limits as the forward
  *  workspace  blasst_select_prefill_backward_workspace_size() bytes, 256-byte
  *             aligned, caller-owned
- * Each gradient is summed in float32 in a fixed order.  P and dS are rounded
- * to bf16 for their tensor-core products, and D = dO . O uses the bf16 o.
+ * Each gradient is summed in float32 in a fixed order.  dK and dV round P and
+ * dS to bf16 for their tensor-core products (2^-8 of each term); dQ takes dS in
+ * two bf16 parts, and D = dO . O, which starts from the bf16 o, is corrected by
+ * the row sums of dS before dQ and dK use it.
  * Asynchronous on `stream`; six kernel launches (five when the key blocks,
  * B * Hkv * ceil(Lkv/128), are at most 148 or more than 32768); allocates
  * nothing.

@@ -334,3 +334,46 @@ def test_training_steps_have_the_same_bits_everywhere(m):
             for name, x, y, z in zip("c sel o lse dq dk dv".split(), a, b, w):
                 assert torch.equal(x, z) and torch.equal(y, z), name
     _clean(m)
+
+
+@pytest.mark.parametrize("Hq,Hkv,Lq,Lkv,causal,n", [
+    (8, 4, 161, 161, True, 3), (4, 1, 300, 700, True, 5),
+    (2, 2, 90, 500, False, 3), (32, 1, 70, 1000, True, 7)])
+def test_backward_dq_is_as_good_as_its_rounding(m, Hq, Hkv, Lq, Lkv, causal, n):
+    """dQ against float64, 2-norms: the rounding of the result itself (bf16 of
+    the exact gradient), and what is off before it by no more than
+    1.3e-4 scale sum_c P_c (|dP_c| + |D|) |k_c| an entry: scores and lse are
+    off by 5e-5 each (sum scale |q k| below 10, cut at 2^-25 of the sum, 21
+    times in each of 8 steps, and the lse's logarithm), dP by the same share
+    of sum |dO v| / |dP|, dS by 2^-16.  (dS as one bf16 number, or D from the
+    bf16 o, would add as much again as the result's rounding.)"""
+    g = _gen(Lq)
+    B, d = 2, 128
+    base = torch.randn(B, Hkv, Lkv // 256 + 1, d, generator=g, device="cuda")
+    k = (0.7 * base.repeat_interleave(256, 2)[:, :, :Lkv] + 0.7 * torch.randn(
+        B, Hkv, Lkv, d, generator=g, device="cuda")).to(BF)
+    q, v = _rand(g, B, Hq, Lq, d), _rand(g, B, Hkv, Lkv, d)
+    do = _rand(g, B, Hq, Lq, d)
+    sel = R.random_selection(torch.Generator().manual_seed(Lq), B, Hkv, Lq,
+                             Lkv, n, causal, "cuda")
+    scale = 1 / math.sqrt(d)
+    o, lse = m.blasst_select_prefill(q, k, v, sel, causal=causal)
+    dq, _, _ = m.blasst_select_prefill_backward(q, k, v, o, lse, do, sel,
+                                                causal=causal)
+    _clean(m)
+    ref = R.attention(q, k, v, sel, scale, causal, do)
+    G = Hq // Hkv
+    kd, vd, dod, od = (t.double().repeat_interleave(r, 1) for t, r in (
+        (k, G), (v, G), (do, 1), (ref["o"], 1)))
+    al = R.allowed(sel, Lq, Lkv, causal).repeat_interleave(G, 1)
+    s = scale * (q.double() @ kd.transpose(-1, -2))
+    p = torch.where(al, torch.exp(s - ref["lse"][..., None]), 0.0)
+    dp = dod @ vd.transpose(-1, -2)
+    D = (dod * od).sum(-1, keepdim=True)
+    before = 1.3e-4 * scale * (p * (dp.abs() + D.abs())) @ kd.abs()
+    rounding = ref["dq"].to(BF).double() - ref["dq"]
+    err = (dq.double() - ref["dq"]).norm()
+    lim = rounding.norm() + before.norm()
+    size = ref["dq"].norm()
+    print(f"{(err / size).item():.5f} of {(lim / size).item():.5f}")
+    assert err <= lim
