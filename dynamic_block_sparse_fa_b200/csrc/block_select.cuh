@@ -837,8 +837,9 @@ cudaError_t launch_block_select_decode(const SelectArgs& a, int B, int nblk,
 // the selection); all scores of the rows stay in shared memory, then each warp
 // selects for two of them.  What bounds it is the selection's instructions,
 // so what counts is warps to hide their latency: 16 rows take 57 KB at 16K
-// keys, three CTAs per SM (215 us for 32 heads on 8 at 16K; 32 rows, two CTAs,
-// 223; 64 rows, one, 336.  B 2, 777 rows on 5K keys: 12.1, 19.8, 19.8).
+// keys, three CTAs per SM (32 heads on 8 at 16K: 201 us.  When this was chosen
+// 215; 32 rows, two CTAs, 223; 64 rows, one, 336.  B 2, 777 rows on 5K keys:
+// 12.1, 19.8, 19.8).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4],
                                          uint32_t b0, uint32_t b1) {

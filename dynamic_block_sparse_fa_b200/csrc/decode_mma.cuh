@@ -223,8 +223,9 @@ __device__ __forceinline__ int sel_compact(const int* sel, int n_sel, int nk,
 // SEL: attention over a.sel's blocks only (paged, dense over those blocks):
 // the CTA lists its (sequence, KV head)'s distinct blocks in shared memory
 // and the splits divide that list instead of the sequence.  Bound by HBM:
-// batch 32 x 8 KV heads, 64 blocks of up to 512, 533 MB in 94 us (0.86 of the
-// measured copy rate).
+// batch 32 x 8 KV heads, 64 blocks of up to 512, 533 MB in 95 us (0.86 of the
+// measured copy rate; 98 us and 0.83 as calls).  P goes into its product as
+// bf16, V's type (2^-8 of each term; the normaliser sums it in float32).
 template <int G, int D, bool PAGED, int BATCH = 1, bool SEL = false>
 __global__ void __launch_bounds__(kDecThreads, 3)
     decode_mma_kernel(const __grid_constant__ DecodeMmaArgs a) {

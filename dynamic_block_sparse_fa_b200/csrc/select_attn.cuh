@@ -192,15 +192,16 @@ struct SelPrefillCfg {
 };
 
 // One query tile per CTA; per step of two blocks S = Q K^T into one of two
-// buffers, P (bf16) into one of two others, O += P V.  A step's softmax is a
-// chain (scores out of tensor memory, maxima, exps, P back) about twice as
-// long as its exps alone keep the MUFU busy, so two groups of 4 warps (thread
-// = row) take the even and the odd steps and overlap: while one group is in
-// its exps the other loads, reduces and stores.  All they share is the row's
-// running max and reference, handed over once per step after three quarters of
-// its exps, so that the groups' exps follow one another.  S of step s + 2 is
-// issued as soon as step s has read its scores, so the chain never waits for
-// the tensor core.
+// buffers, P (bf16, V's type, as the product wants it: 2^-8 of each term; the
+// normaliser sums it in float32) into one of two others, O += P V.  A step's
+// softmax is a chain (scores out of tensor memory, maxima, exps, P back) about
+// twice as long as its exps alone keep the MUFU busy, so two groups of 4 warps
+// (thread = row) take the even and the odd steps and overlap: while one group
+// is in its exps the other loads, reduces and stores.  All they share is the
+// row's running max and reference, handed over once per step after three
+// quarters of its exps, so that the groups' exps follow one another.  S of step
+// s + 2 is issued as soon as step s has read its scores, so the chain never
+// waits for the tensor core.
 //
 // 32 heads on 8, 16K causal, 32 blocks a row: 0.82 ms, the tensor pipe and the
 // MUFU 48% busy each (1024 cycles of either a step, of about 1.9k); 0.9 PFLOP/s
