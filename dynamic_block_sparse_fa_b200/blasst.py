@@ -294,8 +294,8 @@ def blasst_skip_stats_reset(counters: torch.Tensor, stream=None):
 
 def blasst_check_device_error():
     """Returns (status, where): status 0, BLASST_ERR_TIMEOUT (5, a wait gave
-    up) or BLASST_ERR_INVALID_ARG (1, a paged-decode length or page id out of
-    range); for either error `where` is a string naming the first one."""
+    up) or BLASST_ERR_INVALID_ARG (1, a paged call's length or page id, or a
+    selection's block id, out of range); for either error `where` is a string naming the first one."""
     where = ctypes.c_int(0)
     st = _lib.blasst_check_device_error(ctypes.byref(where))
     if st not in (0, 1, 5):
